@@ -329,10 +329,118 @@ int sidbeam_fused_lmhead_step(const sidbeam_trie* trie, int step, const void* hi
                               int32_t* out_node, void* workspace, size_t workspace_bytes,
                               void* stream);
 
+/* ---------------------------------------------------------------- 8-bit lm_head
+ * flashrec 0.1.0, Features (W8A8 FP8 by default; RMSNorm fused with the
+ * quantisation): the lm_head product with both operands in e4m3 and an fp32
+ * scale for every block of SIDBEAM_FP8_BLOCK = 128 elements along d (a weight
+ * scale covers 128 codes x 128 columns). An element stands for q * scale, with
+ *   scale = max(max |y|, 448 * 2^-100) / 448   over the block (fp32),
+ *   q     = e4m3(y * (1 / scale))              round to nearest even,
+ * where 448 is the largest e4m3 value; an all-zero block has scale 2^-100 and
+ * zeros. Inputs must be finite. nb = ceil(d / 128); the last block holds the
+ * remaining columns. d % 16 == 0 (rows of e4m3 start on 16 bytes), d <=
+ * SIDBEAM_MAX_HIDDEN. All calls are asynchronous on `stream`. */
+#define SIDBEAM_FP8_BLOCK 128
+#define SIDBEAM_MAX_HIDDEN 16384
+
+/* residual_rmsnorm_fp8 -- the final norm of M rows, leaving them quantised:
+ *   h = x + residual,  y = h / sqrt(mean_k h_k^2 + eps) * weight
+ * in fp32 (y comes from the unrounded h).
+ *  x             device bf16 [M][d], row-major, 16-byte aligned.
+ *  residual      device bf16 [M][d], or NULL (h = x).
+ *  weight        device bf16 [d], 16-byte aligned.
+ *  eps           finite, >= 0.
+ *  residual_out  device bf16 [M][d]: h rounded, or NULL (not kept). It may be
+ *                the same array as x or as residual.
+ *  hidden_q      device e4m3 [M][d]; hidden_scale device f32 [M][nb].
+ * M = 0 is a no-op. Errors: INVALID_ARG, ALIGNMENT, CUDA. */
+int residual_rmsnorm_fp8(const void* x, const void* residual, const void* weight, float eps,
+                         int M, int d, void* residual_out, void* hidden_q, float* hidden_scale,
+                         void* stream);
+
+/* lmhead_quantize_fp8 -- the lm_head weight laid out once for lmhead_logits_fp8.
+ *  w_sid    device bf16 [V][d], row-major, 16-byte aligned.
+ *  w_q      device e4m3 [V][d]; w_scale device f32 [ceil(V/128)][nb].
+ * Errors: INVALID_ARG, ALIGNMENT, CUDA. */
+int lmhead_quantize_fp8(const void* w_sid, int V, int d, void* w_q, float* w_scale, void* stream);
+
+/* lmhead_logits_fp8 -- lmhead_logits on quantised operands:
+ *   logits[row][c] = sum_b hidden_scale[row][b] * w_scale[c / 128][b]
+ *                          * sum_{k in block b} hidden_q[row][k] * w_q[c][k]
+ * (tcgen05, exact products; each block's sum and the sum over blocks in fp32,
+ * order not specified but the same for every call of the same shape).
+ *  hidden_q     device e4m3 [M][d], hidden_scale device f32 [M][nb].
+ *  w_q          device e4m3 [V][d], w_scale device f32 [ceil(V/128)][nb].
+ *  logits       device [M][ld] of `dtype` (bf16: one rounding of the fp32 sum),
+ *               ld >= V, ld * sizeof(dtype) a multiple of 16; columns past V
+ *               are left as they are. beam_step reads them in place.
+ *  workspace    device, >= 256 bytes, zero-filled before first use (status word).
+ * hidden_q, w_q and logits 16-byte aligned. M = 0 is a no-op. Errors:
+ * INVALID_ARG, ALIGNMENT, WORKSPACE, CUDA. */
+int lmhead_logits_fp8(const void* hidden_q, const float* hidden_scale, const void* w_q,
+                      const float* w_scale, int M, int V, int d, void* logits,
+                      sidbeam_dtype dtype, int64_t ld, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+/* ---------------------------------------------------------------- beam attention
+ * beam_attention -- attention of a step's beam rows over their request's prompt
+ * cache and their own ancestors (OneLA, paper summary, section 3.3: children
+ * refer to their parents' records, nothing is copied). The beams of a request
+ * form a tree whose links are the back-pointers that beam_step writes; the
+ * prompt is shared by the whole tree. Row (r, b) with `level` steps behind it
+ * attends cache_len[r] prompt tokens and `level` beam tokens: slot a_u of level
+ * u for u = level-1 .. 0, where a_{level-1} = b and a_{u-1} = bp_parent[u][r][a_u].
+ *   out[row][h] = sum_j softmax_j(scale * <q[row][h], k_j>) v_j
+ * with the keys and values of head h / (H / Hkv). Products bf16 on the tensor
+ * cores, scores, maxima, sums and the output's accumulation in fp32; the weights
+ * are rounded to bf16 before they meet the cached values.
+ *  q            device bf16 [R*B][H][D]; a row starts q_row_stride elements after
+ *               the one before (>= H*D, % 8 == 0; a slice of a wider projection
+ *               is fine). Rows are request-major, row = r * B + b.
+ *  k_cache,     device bf16 [n_pages][page_size][Hkv][D]; page and token strides
+ *  v_cache      in elements, both % 8 == 0 and the same for both arrays.
+ *  page_table   device i32 [R][pages_per_request] of page numbers: token i of
+ *               request r is row i % page_size of page page_table[r][i / page_size];
+ *               page_size is then a power of two in [16, 65536]. Only the pages
+ *               that hold cache_len[r] tokens are read; the rest of the table
+ *               may hold anything. NULL: one slab per request (n_pages = R,
+ *               page_size = its capacity, any >= 1; pages_per_request ignored).
+ *               A page number outside [0, n_pages) reads as a page of zeros and
+ *               sets the status word (DEVICE_CHECK).
+ *  cache_len    device i32 [R], 0 <= cache_len[r] <= capacity (pages_per_request *
+ *               page_size). Values outside are clamped and set the status word.
+ *               Cache rows past cache_len may hold anything, NaN included.
+ *  level        beam steps behind the rows, 0..SIDBEAM_MAX_DEPTH; 0: the rows see
+ *               the prompt only (the first step, B = 1; bp_parent, k_beam, v_beam
+ *               are then ignored).
+ *  bp_parent    device i32 [level][R][B], the first `level` slices of a search's
+ *               history. A row one of whose links lies outside [0, B) (bp_parent[0]:
+ *               < 0) is a dead beam: its output is zero.
+ *  k_beam,      device bf16 [level][R*B][Hkv][D]: the keys and values of the token
+ *  v_beam       each beam chose at each level.
+ *  R, B         requests and rows per request, B <= SIDBEAM_MAX_BEAM.
+ *  H, Hkv, D    query heads, key/value heads (H % Hkv == 0, H / Hkv <= 128), head
+ *               size 64 or 128.
+ *  scale        finite; usually 1 / sqrt(D).
+ *  out          device bf16 [R*B][H][D] with out_row_stride (as q_row_stride). A
+ *               row that attends nothing (no token, level 0) is zero. Must not
+ *               overlap the inputs.
+ *  workspace    device, >= 256 bytes, 256-byte aligned, zero-filled before first
+ *               use (status word).
+ * Pointers 16-byte aligned. Asynchronous on `stream`. Errors: INVALID_ARG,
+ * ALIGNMENT, WORKSPACE, CUDA. */
+int beam_attention(const void* q, int64_t q_row_stride, const void* k_cache, const void* v_cache,
+                   int64_t page_stride, int64_t token_stride, int n_pages, int page_size,
+                   const int32_t* page_table, int pages_per_request, const int32_t* cache_len,
+                   int level, const int32_t* bp_parent, const void* k_beam, const void* v_beam,
+                   int R, int B, int H, int Hkv, int D, float scale, void* out,
+                   int64_t out_row_stride, void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---------------------------------------------------------------- status
  * sidbeam_get_device_status -- synchronises `stream`, reads and clears the
  * status word that beam_step / catalog_score_topk keep at the start of
- * `workspace`; returns SIDBEAM_OK, DEVICE_CHECK (a bad node id was seen) or
+ * `workspace` (the 8-bit product and beam_attention keep theirs there too);
+ * returns SIDBEAM_OK, DEVICE_CHECK (a bad node id, page number or length) or
  * TIMEOUT (a bounded wait inside a kernel gave up). */
 int sidbeam_get_device_status(void* workspace, void* stream);
 

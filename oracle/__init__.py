@@ -45,3 +45,6 @@ from .beam import (  # noqa: F401
 from .catalog import catalog_score_topk  # noqa: F401
 from .lmhead import lmhead_logits, fused_lmhead_step  # noqa: F401
 from .gumbel import beam_step_gumbel, gumbel, philox4x32_10  # noqa: F401
+from . import fp8  # noqa: F401
+from . import attention  # noqa: F401
+from .attention import beam_attention  # noqa: F401

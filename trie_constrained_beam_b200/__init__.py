@@ -7,6 +7,7 @@ from . import native  # noqa: F401
 from .native import (  # noqa: F401
     SidbeamError,
     Trie,
+    beam_attention,
     beam_finalize,
     beam_step,
     beam_step_gumbel,
@@ -20,6 +21,9 @@ from .native import (  # noqa: F401
     fused_lmhead_step,
     fused_lmhead_workspace_size,
     lmhead_logits,
+    lmhead_logits_fp8,
+    lmhead_quantize_fp8,
+    residual_rmsnorm_fp8,
     sid_trie_build,
     sid_trie_info,
     sid_trie_leaf_codes,
@@ -28,6 +32,6 @@ from .native import (  # noqa: F401
     sidbeam_last_error,
     sidbeam_version,
 )
-from .search import BeamSearch  # noqa: F401
+from .search import BeamSearch, LmheadFp8  # noqa: F401
 
 __version__ = "0.1.0"

@@ -329,6 +329,8 @@ extern "C" int sidbeam_get_device_status(void* workspace, void* stream) {
   }
   if (word & kStatusTimeout)
     return set_error(SIDBEAM_ERR_TIMEOUT, "a bounded wait inside a kernel gave up");
+  if (word & kStatusBadCache)
+    return set_error(SIDBEAM_ERR_DEVICE_CHECK, "a page number or a length was outside the cache");
   if (word & kStatusBadNode)
     return set_error(SIDBEAM_ERR_DEVICE_CHECK, "a parent node id was outside the trie level");
   return SIDBEAM_OK;

@@ -1,0 +1,552 @@
+// SID-range lm_head with both operands in e4m3 and a scale per 128 elements
+// along d, on the 5th-generation tensor cores.
+//
+// flashrec 0.1.0 (PyPI page), Features: W8A8 FP8; Features > Decoding ("SID
+// constraint"): the lm_head covers the SID token range only.
+//
+//   z[m][c] = sum_b sa[m][b] * sw[c / 128][b] * (sum_{k in b} q[m][k] * w[c][k])
+//
+// The scales change every 128 columns of d, so the tensor core cannot carry one
+// accumulator through the whole dot product: each block's sum (4 MMAs of K = 32)
+// goes to a TMEM accumulator of its own, and the epilogue warps add it, times
+// the row's and the code block's scale, to fp32 registers while the MMAs of the
+// next block run into the other accumulators.
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "internal.h"
+#include "tcgen05.cuh"
+
+namespace sidbeam {
+namespace {
+
+using namespace dev;
+
+constexpr int kBlock = SIDBEAM_FP8_BLOCK;  // 128 e4m3: 128 bytes, one swizzle row
+constexpr float kZero = 0.f;
+
+// Instruction descriptor of kind::f8f6f4: fp32 accumulator, e4m3 A and B (format
+// 0), both K-major, M = 128.
+constexpr uint32_t idesc_f8(int n) {
+  return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+struct Fp8Args {
+  int M, V, nb;               // rows, codes, blocks of 128 along d
+  const float* sa;            // [M][nb]
+  const float* sw;            // [ceil(V/128)][nb]
+  void* out;                  // [M][ld]
+  int64_t ld;
+  uint32_t* status;
+};
+
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                     uint32_t* status) {
+  return bounded_wait(bar, parity, abort, status, kStatusTimeout);
+}
+
+// ------------------------------------------------------------ many rows
+// Persistent over 128 x 256 tiles. Warp 0 loads (TMA), warp 1 issues MMAs, warps
+// 2-9 are the epilogue: the warp pair of a TMEM lane quarter takes 128 columns
+// each (one scale block), 128 fp32 registers per thread.
+constexpr int kTileM = 128;
+constexpr int kTileN = 256;
+constexpr int kStages = 4;
+constexpr int kABytes = kTileM * kBlock;
+constexpr int kStageBytes = (kTileM + kTileN) * kBlock;  // 48 KiB
+constexpr int kThreads = 320;
+constexpr int kEpiWarps = 8;
+constexpr int kChunk = 128;                              // bytes of a row per store chunk
+constexpr int kStore = kEpiWarps * 32 * kChunk;          // 32 KiB
+constexpr int kSmem = kStages * kStageBytes + kStore + 1024 + 256;
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_h,
+                    const __grid_constant__ CUtensorMap map_w, const Fp8Args a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* store = smem + kStages * kStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(store + kStore);
+  uint64_t* empty = full + kStages;
+  uint64_t* acc_full = empty + kStages;  // [2]
+  uint64_t* acc_empty = acc_full + 2;    // [2]
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int m_tiles = (a.M + kTileM - 1) / kTileM;
+  const int n_tiles = (a.V + kTileN - 1) / kTileN;
+  const int tiles = m_tiles * n_tiles;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      prefetch_map(&map_h);
+      prefetch_map(&map_w);
+      uint32_t it = 0;
+      for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const int nt = t / m_tiles, mt = t - nt * m_tiles;
+        for (int k = 0; k < a.nb; ++k, ++it) {
+          const int s = static_cast<int>(it % kStages);
+          if (it >= static_cast<uint32_t>(kStages) &&
+              !wait(&empty[s], ((it / kStages) - 1) & 1u, abort_flag, a.status))
+            goto loaded;
+          uint8_t* st = smem + s * kStageBytes;
+          mbar_arrive_expect_tx(&full[s], kStageBytes);
+          tma_load_2d(st, &map_h, k * kBlock, mt * kTileM, &full[s]);
+          tma_load_2d(st + kABytes, &map_w, k * kBlock, nt * kTileN, &full[s]);
+        }
+      }
+    loaded:
+      for (uint32_t j = it > static_cast<uint32_t>(kStages) ? it - kStages : 0u; j < it; ++j)
+        drain_wait(&full[j % kStages], (j / kStages) & 1u);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+        for (int k = 0; k < a.nb; ++k, ++it) {
+          const int s = static_cast<int>(it % kStages);
+          const uint32_t ab = it & 1u;
+          if ((it >= 2 && !wait(&acc_empty[ab], ((it >> 1) - 1) & 1u, abort_flag, a.status)) ||
+              !wait(&full[s], (it / kStages) & 1u, abort_flag, a.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_addr(smem + s * kStageBytes);
+          const uint32_t sb = sa + kABytes;
+#pragma unroll
+          for (int kk = 0; kk < kBlock / 32; ++kk)
+            umma_f8(tmem + ab * kTileN, smem_desc(sa + kk * 32), smem_desc(sb + kk * 32),
+                    idesc_f8(kTileN), kk > 0 ? 1u : 0u);
+          umma_commit(&empty[s]);
+          umma_commit(&acc_full[ab]);
+        }
+      }
+      umma_commit(drain);
+      drain_wait(drain, 0u);
+    }
+  } else {
+    const int quarter = warp & 3;       // TMEM lanes 32 * quarter .. + 31
+    const int half = (warp - 2) >> 2;   // columns 128 * half .. + 127 of the tile
+    uint8_t* chunk = store + (warp - 2) * 32 * kChunk;
+    uint32_t it = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+      const int nt = t / m_tiles, mt = t - nt * m_tiles;
+      const int row = mt * kTileM + quarter * 32 + lane;
+      const int n0 = nt * kTileN + half * kBlock;
+      const float* sa = a.sa + static_cast<int64_t>(min(row, a.M - 1)) * a.nb;
+      const float* sw = a.sw + static_cast<int64_t>(min(n0, a.V - 1) / kBlock) * a.nb;
+      uint64_t acc[64];
+      const uint64_t zero = pack_f32x2(kZero, kZero);
+#pragma unroll
+      for (int e = 0; e < 64; ++e) acc[e] = zero;
+      float s = sa[0] * sw[0];
+      for (int k = 0; k < a.nb; ++k, ++it) {
+        const uint32_t ab = it & 1u;
+        const uint64_t s2 = pack_f32x2(s, s);
+        if (k + 1 < a.nb) s = sa[k + 1] * sw[k + 1];
+        if (!wait(&acc_full[ab], (it >> 1) & 1u, abort_flag, a.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t taddr = tmem + ab * kTileN + half * kBlock +
+                               (static_cast<uint32_t>(quarter * 32) << 16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t v[32];
+          tmem_ld32(taddr + j * 32, v);
+          if (j == 3) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[ab]);
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            acc[j * 16 + e] =
+                fma_f32x2(pack_f32x2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), s2,
+                          acc[j * 16 + e]);
+        }
+      }
+      if (!ok) break;
+      // 128-byte pieces of the warp's 32 rows through shared memory (16-byte
+      // units, unit u of row l at u ^ (l & 7)), so that global stores cover
+      // whole lines.
+      constexpr int kCols = kChunk / static_cast<int>(sizeof(T));  // 32 fp32 or 64 bf16
+#pragma unroll
+      for (int j = 0; j < kBlock / kCols; ++j) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          uint4 w;
+          float f[8];
+          if constexpr (sizeof(T) == 4) {
+            unpack_f32x2(acc[j * 16 + u * 2], f[0], f[1]);
+            unpack_f32x2(acc[j * 16 + u * 2 + 1], f[2], f[3]);
+            w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                           __float_as_uint(f[3]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) unpack_f32x2(acc[j * 32 + u * 4 + e], f[2 * e], f[2 * e + 1]);
+            w = make_uint4(bf16x2(f[0], f[1]), bf16x2(f[2], f[3]), bf16x2(f[4], f[5]),
+                           bf16x2(f[6], f[7]));
+          }
+          *reinterpret_cast<uint4*>(chunk + lane * kChunk + ((u ^ (lane & 7)) << 4)) = w;
+        }
+        __syncwarp();
+        constexpr int kUnit = 16 / static_cast<int>(sizeof(T));
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          const int l = p * 4 + (lane >> 3), u = lane & 7;
+          const uint4 w = *reinterpret_cast<const uint4*>(chunk + l * kChunk + ((u ^ (l & 7)) << 4));
+          const int r = mt * kTileM + quarter * 32 + l;
+          const int c = n0 + j * kCols + u * kUnit;
+          if (r < a.M) {
+            T* o = static_cast<T*>(a.out) + static_cast<int64_t>(r) * a.ld + c;
+            if (c + kUnit <= a.V) {
+              *reinterpret_cast<uint4*>(o) = w;
+            } else {
+              T f[kUnit];
+              *reinterpret_cast<uint4*>(f) = w;
+#pragma unroll
+              for (int e = 0; e < kUnit; ++e)
+                if (c + e < a.V) o[e] = f[e];
+            }
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_free(tmem, 512);
+}
+
+// ------------------------------------------------------------ few rows
+// The operands change places: a tile is 128 codes (M of the MMA) x NB rows, so a
+// handful of rows does not leave most of a 128-row tile empty, and the weight,
+// which is all that counts here, is read once. The CTAs of a cluster share a
+// tile and split d; each adds up its part in registers, and the parts meet
+// through distributed shared memory in rank order (the same sum every time).
+constexpr int kRowThreads = 192;  // TMA warp, MMA warp, 4 epilogue warps
+
+template <int NB>
+struct RowPlan {
+  static constexpr int kStage = (kTileM + NB) * kBlock;
+  static constexpr int kAcc = NB >= 128 ? 4 : 8;  // TMEM accumulators of NB columns
+  static constexpr int kTmemCols = NB * kAcc < 32 ? 32 : NB * kAcc;
+};
+
+template <int NB, typename T>
+__global__ void __launch_bounds__(kRowThreads, 1)
+    fp8_rows_kernel(const __grid_constant__ CUtensorMap map_h,
+                    const __grid_constant__ CUtensorMap map_w, const Fp8Args a, int split,
+                    int stages) {
+  using P = RowPlan<NB>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  __shared__ uint64_t full[8], empty[8], acc_full[8], acc_empty[8], drain;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rank = split > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int tile = blockIdx.x / split;
+  const int m0 = blockIdx.y * NB;
+  const int kb0 = a.nb * rank / split, kb1 = a.nb * (rank + 1) / split;
+  const int n = kb1 - kb0;
+  float* table = reinterpret_cast<float*>(smem + stages * P::kStage);  // [n][NB]
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 8; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+      mbar_init(&acc_full[s], 1);
+      mbar_init(&acc_empty[s], 4);
+    }
+    mbar_init(&drain, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(&tmem_slot, P::kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  float acc[NB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j) acc[j] = 0.f;
+  if (warp == 0) {
+    if (lane == 0) {
+      int i = 0;
+      for (; i < n; ++i) {
+        const int s = i % stages;
+        if (i >= stages && !wait(&empty[s], ((i / stages) - 1) & 1u, &abort_flag, a.status)) break;
+        uint8_t* st = smem + s * P::kStage;
+        mbar_arrive_expect_tx(&full[s], P::kStage);
+        tma_load_2d(st, &map_w, (kb0 + i) * kBlock, tile * kTileM, &full[s]);
+        tma_load_2d(st + kABytes, &map_h, (kb0 + i) * kBlock, m0, &full[s]);
+      }
+      for (int j = max(0, i - stages); j < i; ++j)
+        drain_wait(&full[j % stages], (j / stages) & 1u);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      for (int i = 0; i < n; ++i) {
+        const int s = i % stages, ab = i % P::kAcc;
+        if ((i >= P::kAcc &&
+             !wait(&acc_empty[ab], ((i / P::kAcc) - 1) & 1u, &abort_flag, a.status)) ||
+            !wait(&full[s], (i / stages) & 1u, &abort_flag, a.status))
+          break;
+        tc_fence_after();
+        const uint32_t sw = smem_addr(smem + s * P::kStage);
+#pragma unroll
+        for (int kk = 0; kk < kBlock / 32; ++kk)
+          umma_f8(tmem + ab * NB, smem_desc(sw + kk * 32), smem_desc(sw + kABytes + kk * 32),
+                  idesc_f8(NB), kk > 0 ? 1u : 0u);
+        umma_commit(&empty[s]);
+        umma_commit(&acc_full[ab]);
+      }
+      umma_commit(&drain);
+      drain_wait(&drain, 0u);
+    }
+  } else {
+    // table[i][j] = the factor of row m0 + j in block kb0 + i for this tile.
+    const int e0 = threadIdx.x - 64;
+    for (int e = e0; e < n * NB; e += 128) {
+      const int j = e / n, i = e - j * n;
+      table[i * NB + j] = m0 + j < a.M
+                              ? a.sa[static_cast<int64_t>(m0 + j) * a.nb + kb0 + i] *
+                                    a.sw[static_cast<int64_t>(tile) * a.nb + kb0 + i]
+                              : 0.f;
+    }
+    named_sync(1, 128);
+    const int quarter = warp & 3;
+    for (int i = 0; i < n; ++i) {
+      const int ab = i % P::kAcc;
+      if (!wait(&acc_full[ab], (i / P::kAcc) & 1u, &abort_flag, a.status)) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem + ab * NB + (static_cast<uint32_t>(quarter * 32) << 16);
+#pragma unroll
+      for (int j0 = 0; j0 < NB; j0 += 16) {
+        uint32_t v[16];
+        tmem_ld16(taddr + j0, v);
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(table + i * NB + j0 + j);
+          acc[j0 + j] = fmaf(__uint_as_float(v[j]), f.x, acc[j0 + j]);
+          acc[j0 + j + 1] = fmaf(__uint_as_float(v[j + 1]), f.y, acc[j0 + j + 1]);
+          acc[j0 + j + 2] = fmaf(__uint_as_float(v[j + 2]), f.z, acc[j0 + j + 2]);
+          acc[j0 + j + 3] = fmaf(__uint_as_float(v[j + 3]), f.w, acc[j0 + j + 3]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[ab]);
+    }
+  }
+  // The stages are free now (every block has been multiplied).
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_free(tmem, P::kTmemCols);
+  float* part = reinterpret_cast<float*>(smem);  // [NB][128]
+  const int c_local = (warp & 3) * 32 + lane;
+  const int c = tile * kTileM + c_local;
+  T* out = static_cast<T*>(a.out) + c;
+  if (split == 1) {
+    if (warp >= 2 && c < a.V) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        if (m0 + j < a.M) out[static_cast<int64_t>(m0 + j) * a.ld] = static_cast<T>(acc[j]);
+    }
+    return;
+  }
+  if (warp >= 2) {
+#pragma unroll
+    for (int j = 0; j < NB; ++j) part[j * 128 + c_local] = acc[j];
+  }
+  cluster_sync();
+  if (warp >= 2 && c < a.V) {
+    const int rows = min(NB, a.M - m0);
+    for (int j = rank; j < rows; j += split) {
+      float z = 0.f;
+      for (int p = 0; p < split; ++p) z += ld_peer(peer_addr(&part[j * 128 + c_local], p));
+      out[static_cast<int64_t>(m0 + j) * a.ld] = static_cast<T>(z);
+    }
+  }
+  cluster_sync();  // no CTA leaves while another still reads its part
+}
+
+// ------------------------------------------------------------ host side
+// 2-D e4m3 tensor map over a row-major [rows][cols] matrix, box [box_rows][128].
+bool make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(kBlock), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Opts `kernel` into `smem` bytes of shared memory, once per device and kernel
+// (`done`: that kernel's flags).
+template <typename K>
+cudaError_t opt_in(K kernel, int smem, bool (&done)[64]) {
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+  return e;
+}
+
+template <typename T>
+int launch_gemm(const void* h, const void* w, const Fp8Args& a, int d, cudaStream_t stream) {
+  CUtensorMap mh, mw;
+  if (!make_map(&mh, h, a.M, d, kTileM) || !make_map(&mw, w, a.V, d, kTileN))
+    return set_error(SIDBEAM_ERR_CUDA, "lmhead_logits_fp8: tensor map encoding failed");
+  static bool done[64] = {};
+  cudaError_t e = opt_in(fp8_gemm_kernel<T>, kSmem, done);
+  if (e != cudaSuccess) return cuda_error(e, "lmhead_logits_fp8: cudaFuncSetAttribute");
+  const int64_t tiles =
+      static_cast<int64_t>((a.M + kTileM - 1) / kTileM) * ((a.V + kTileN - 1) / kTileN);
+  const int grid = static_cast<int>(std::min<int64_t>(tiles, device_sm_count()));
+  fp8_gemm_kernel<T><<<grid, kThreads, kSmem, stream>>>(mh, mw, a);
+  e = cudaGetLastError();
+  return e == cudaSuccess ? SIDBEAM_OK : cuda_error(e, "lmhead_logits_fp8: launch");
+}
+
+template <int NB, typename T>
+int launch_rows(const void* h, const void* w, const Fp8Args& a, int d, cudaStream_t stream) {
+  using P = RowPlan<NB>;
+  CUtensorMap mh, mw;
+  if (!make_map(&mh, h, a.M, d, NB) || !make_map(&mw, w, a.V, d, kTileM))
+    return set_error(SIDBEAM_ERR_CUDA, "lmhead_logits_fp8: tensor map encoding failed");
+  const int tiles = (a.V + kTileM - 1) / kTileM;
+  const int groups = (a.M + NB - 1) / NB;
+  const int sms = device_sm_count();
+  // CTAs per tile: up to 8 while the grid fits the SMs and every CTA has a block.
+  int split = 1;
+  while (split < 8 && split * 2 <= a.nb && tiles * groups * split * 2 <= sms) split *= 2;
+  const int n = (a.nb + split - 1) / split;
+  const int table = n * NB * 4;
+  const int budget = 224 * 1024 - 1024 - table;
+  const int stages = std::max(2, std::min({8, n, budget / P::kStage}));
+  const int smem = 1024 + std::max(stages * P::kStage + table, NB * 128 * 4);
+  static bool done[64] = {};
+  cudaError_t e = opt_in(fp8_rows_kernel<NB, T>, 224 * 1024, done);
+  if (e != cudaSuccess) return cuda_error(e, "lmhead_logits_fp8: cudaFuncSetAttribute");
+  cudaLaunchConfig_t lc{};
+  lc.gridDim = dim3(static_cast<unsigned>(tiles * split), static_cast<unsigned>(groups));
+  lc.blockDim = dim3(kRowThreads);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  e = cudaLaunchKernelEx(&lc, fp8_rows_kernel<NB, T>, mh, mw, a, split, stages);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return e == cudaSuccess ? SIDBEAM_OK : cuda_error(e, "lmhead_logits_fp8: launch");
+}
+
+template <typename T>
+int launch(const void* h, const void* w, const Fp8Args& a, int d, cudaStream_t stream) {
+  if (a.M <= 16) return launch_rows<16, T>(h, w, a, d, stream);
+  if (a.M <= 32) return launch_rows<32, T>(h, w, a, d, stream);
+  if (a.M <= 64) return launch_rows<64, T>(h, w, a, d, stream);
+  if (a.M <= 128) return launch_rows<128, T>(h, w, a, d, stream);
+  return launch_gemm<T>(h, w, a, d, stream);
+}
+
+bool misaligned(const void* p, uintptr_t to) {
+  return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0;
+}
+
+}  // namespace
+}  // namespace sidbeam
+
+using namespace sidbeam;
+
+extern "C" int lmhead_logits_fp8(const void* hidden_q, const float* hidden_scale, const void* w_q,
+                                 const float* w_scale, int M, int V, int d, void* logits,
+                                 sidbeam_dtype dtype, int64_t ld, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  if (dtype != SIDBEAM_F32 && dtype != SIDBEAM_BF16)
+    return set_error(SIDBEAM_ERR_INVALID_ARG, "lmhead_logits_fp8: unknown dtype %d",
+                     static_cast<int>(dtype));
+  if (M < 0 || V < 1 || V > SIDBEAM_MAX_V || d < 16 || d > SIDBEAM_MAX_HIDDEN || (d & 15) != 0)
+    return set_error(SIDBEAM_ERR_INVALID_ARG,
+                     "lmhead_logits_fp8: bad shape M=%d V=%d d=%d (d a multiple of 16, at most %d)",
+                     M, V, d, SIDBEAM_MAX_HIDDEN);
+  if (M == 0) return SIDBEAM_OK;
+  if (!hidden_q || !hidden_scale || !w_q || !w_scale || !logits)
+    return set_error(SIDBEAM_ERR_INVALID_ARG, "lmhead_logits_fp8: NULL pointer argument");
+  const int esize = dtype == SIDBEAM_BF16 ? 2 : 4;
+  if (ld < V)
+    return set_error(SIDBEAM_ERR_INVALID_ARG, "lmhead_logits_fp8: ld=%lld < V=%d",
+                     static_cast<long long>(ld), V);
+  if (misaligned(hidden_q, 16) || misaligned(w_q, 16) || misaligned(logits, 16) ||
+      misaligned(hidden_scale, 4) || misaligned(w_scale, 4) || (ld * esize) % 16 != 0)
+    return set_error(SIDBEAM_ERR_ALIGNMENT,
+                     "lmhead_logits_fp8: hidden_q, w_q and logits must be 16-byte aligned, "
+                     "ld * sizeof(dtype) %% 16 == 0");
+  if (!workspace || workspace_bytes < 256 || misaligned(workspace, 256))
+    return set_error(SIDBEAM_ERR_WORKSPACE,
+                     "lmhead_logits_fp8: workspace of >= 256 bytes, 256-byte aligned");
+  Fp8Args a{};
+  a.M = M;
+  a.V = V;
+  a.nb = (d + kBlock - 1) / kBlock;
+  a.sa = hidden_scale;
+  a.sw = w_scale;
+  a.out = logits;
+  a.ld = ld;
+  a.status = static_cast<uint32_t*>(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return dtype == SIDBEAM_BF16 ? launch<__nv_bfloat16>(hidden_q, w_q, a, d, s)
+                               : launch<float>(hidden_q, w_q, a, d, s);
+}

@@ -44,8 +44,12 @@ EXPORTED = (
     "sidbeam_last_error", "sidbeam_version", "beam_step_noalloc", "lmhead_logits",
     "fused_lmhead_workspace_size", "sidbeam_fused_lmhead_step", "beam_step_ex",
     "beam_step_skipped_rows", "catalog_score_topk_sim", "beam_step_gumbel",
-    "beam_step_gumbel_workspace_size",
+    "beam_step_gumbel_workspace_size", "residual_rmsnorm_fp8", "lmhead_quantize_fp8",
+    "lmhead_logits_fp8", "beam_attention",
 )
+
+FP8_BLOCK = 128      # SIDBEAM_FP8_BLOCK: elements that share a scale
+MAX_HIDDEN = 16384   # SIDBEAM_MAX_HIDDEN
 
 STEP_SKIP_ROWS = 1  # SIDBEAM_STEP_SKIP_ROWS
 
@@ -99,6 +103,11 @@ def load():
     L.fused_lmhead_workspace_size.restype = SZ
     L.sidbeam_fused_lmhead_step.argtypes = [P, I32, P, P, I32, P, P, I32, I32, I32, I32, P, P, P,
                                             P, P, SZ, P]
+    L.residual_rmsnorm_fp8.argtypes = [P, P, P, ctypes.c_float, I32, I32, P, P, P, P]
+    L.lmhead_quantize_fp8.argtypes = [P, I32, I32, P, P, P]
+    L.lmhead_logits_fp8.argtypes = [P, P, P, P, I32, I32, I32, P, I32, I64, P, SZ, P]
+    L.beam_attention.argtypes = [P, I64, P, P, I64, I64, I32, I32, P, I32, P, I32, P, P, P, I32,
+                                 I32, I32, I32, I32, ctypes.c_float, P, I64, P, SZ, P]
     L.sidbeam_last_error.argtypes = []
     L.sidbeam_last_error.restype = ctypes.c_char_p
     L.sidbeam_version.argtypes = []
@@ -107,7 +116,8 @@ def load():
                  "beam_step", "beam_step_noalloc", "beam_finalize", "catalog_score_topk",
                  "sidbeam_get_device_status", "lmhead_logits", "sidbeam_fused_lmhead_step",
                  "beam_step_ex", "beam_step_skipped_rows", "catalog_score_topk_sim",
-                 "beam_step_gumbel"):
+                 "beam_step_gumbel", "residual_rmsnorm_fp8", "lmhead_quantize_fp8",
+                 "lmhead_logits_fp8", "beam_attention"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
@@ -331,6 +341,163 @@ def fused_lmhead_step(trie, step, hidden, w_sid, parent_scores, parent_nodes, R,
         _ptr(out_parent), _ptr(out_code), _ptr(out_node), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream))
     _check(rc)
+
+
+def _need(t, name, dtype, shape=None, optional=False):
+    """Checks a tensor argument; returns its device address (None for an optional
+    argument left out). ``shape``: the exact shape of a contiguous tensor."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is missing")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} dtype {t.dtype} is not {dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} is not on a CUDA device")
+    if shape is not None and (tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}, "
+                         f"got {tuple(t.shape)} with strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _same_device(first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+
+
+def _run_on(t, stream, fn, *args):
+    """Calls a C entry on the device of tensor `t`: on `stream`, or on that
+    device's current stream."""
+    import torch
+    index = t.device.index
+    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if index == torch._C._cuda_getDevice():
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, s)
+    if rc != SIDBEAM_OK:
+        raise SidbeamError(rc, sidbeam_last_error())
+
+
+def residual_rmsnorm_fp8(x, residual, weight, eps, residual_out, hidden_q, hidden_scale,
+                         stream=None):
+    """h = x + residual; y = h / sqrt(mean h^2 + eps) * weight, left in 8 bits:
+    hidden_q e4m3 [M][d] with hidden_scale f32 [M][ceil(d/128)], a scale per 128
+    columns. x, residual (or None) bf16 [M][d], weight bf16 [d]; residual_out
+    (or None) receives h in bf16 and may be x or residual itself."""
+    import torch
+    M, d = x.shape
+    bf16 = torch.bfloat16
+    args = (_need(x, "x", bf16, (M, d)), _need(residual, "residual", bf16, (M, d), True),
+            _need(weight, "weight", bf16, (d,)), float(eps), M, d,
+            _need(residual_out, "residual_out", bf16, (M, d), True),
+            _need(hidden_q, "hidden_q", torch.float8_e4m3fn, (M, d)),
+            _need(hidden_scale, "hidden_scale", torch.float32, (M, -(-d // FP8_BLOCK))))
+    _same_device(x, residual, weight, residual_out, hidden_q, hidden_scale)
+    _run_on(x, stream, load().residual_rmsnorm_fp8, *args)
+
+
+def lmhead_quantize_fp8(w_sid, w_q, w_scale, stream=None):
+    """The lm_head weight in 8 bits for lmhead_logits_fp8: w_sid bf16 [V][d] ->
+    w_q e4m3 [V][d], w_scale f32 [ceil(V/128)][ceil(d/128)]."""
+    import torch
+    V, d = w_sid.shape
+    args = (_need(w_sid, "w_sid", torch.bfloat16, (V, d)), V, d,
+            _need(w_q, "w_q", torch.float8_e4m3fn, (V, d)),
+            _need(w_scale, "w_scale", torch.float32, (-(-V // FP8_BLOCK), -(-d // FP8_BLOCK))))
+    _same_device(w_sid, w_q, w_scale)
+    _run_on(w_sid, stream, load().lmhead_quantize_fp8, *args)
+
+
+def lmhead_logits_fp8(hidden_q, hidden_scale, w_q, w_scale, out, workspace, stream=None):
+    """lmhead_logits on operands in 8 bits: out[row][c] = sum over blocks of 128
+    columns of hidden_scale[row][b] * w_scale[c // 128][b] * <hidden_q, w_q>_b
+    (fp32 accumulation). out f32 or bf16 [M][V], rows out.stride(0) apart."""
+    import torch
+    M, d = hidden_q.shape
+    V = w_q.shape[0]
+    nb = -(-d // FP8_BLOCK)
+    e4m3, f32 = torch.float8_e4m3fn, torch.float32
+    if tuple(out.shape) != (M, V) or (V > 1 and out.stride(1) != 1):
+        raise ValueError(f"out must be [{M}, {V}] with unit column stride, got "
+                         f"{tuple(out.shape)} with strides {out.stride()}")
+    # The stride of a single row means nothing: any aligned one serves.
+    ld = out.stride(0) if M > 1 else -(-V // 8) * 8
+    args = (_need(hidden_q, "hidden_q", e4m3, (M, d)),
+            _need(hidden_scale, "hidden_scale", f32, (M, nb)), _need(w_q, "w_q", e4m3, (V, d)),
+            _need(w_scale, "w_scale", f32, (-(-V // FP8_BLOCK), nb)), M, V, d,
+            _need(out, "out", out.dtype), _dtype_code(out), ld,
+            _need(workspace, "workspace", workspace.dtype),
+            workspace.numel() * workspace.element_size())
+    _same_device(hidden_q, hidden_scale, w_q, w_scale, out, workspace)
+    _run_on(hidden_q, stream, load().lmhead_logits_fp8, *args)
+
+
+def _heads(t, name, lead, D=None):
+    """A bf16 [..., heads, D] tensor whose last two axes are contiguous."""
+    import torch
+    if t.dim() != lead + 2 or (D is not None and t.shape[-1] != D):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}")
+    if t.stride(-1) != 1 or (t.shape[-2] > 1 and t.stride(-2) != t.shape[-1]):
+        raise ValueError(f"{name}: heads must be contiguous, got strides {t.stride()}")
+    return _need(t, name, torch.bfloat16)
+
+
+def beam_attention(q, k_cache, v_cache, cache_len, out, workspace, page_table=None, level=0,
+                   k_beam=None, v_beam=None, bp_parent=None, scale=None, stream=None):
+    """Attention of beam rows over their request's prompt cache and, for level > 0,
+    their own ancestors through the back-pointer history.
+
+    q, out      bf16 [R*B, H, D] (rows request-major, any row stride)
+    k_cache,    bf16 [R, capacity, Hkv, D], or with page_table int32 [R, pages]
+    v_cache     [n_pages, page_size, Hkv, D]; the same strides for both
+    cache_len   int32 [R] prompt tokens of each request
+    level       steps behind the rows; the first `level` slices of bp_parent
+                int32 [depth, R, B] and of k_beam, v_beam bf16 [depth, R*B, Hkv, D]
+    scale       default D ** -0.5
+    """
+    import torch
+    i32 = torch.int32
+    rows, H, D = q.shape
+    R = cache_len.shape[0]
+    B = rows // R if R else 0
+    Hkv = k_cache.shape[2]
+    if R < 1 or B * R != rows:
+        raise ValueError(f"{rows} query rows for {R} requests")
+    if v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride():
+        raise ValueError("k_cache and v_cache differ in shape or strides")
+    if out.shape != q.shape:
+        raise ValueError("out and q differ in shape")
+    n_pages, page_size = k_cache.shape[0], k_cache.shape[1]
+    table, per, kb, vb, bp = None, 0, None, None, None
+    if page_table is not None:
+        per = page_table.shape[1] if page_table.dim() == 2 else 0
+        table = _need(page_table, "page_table", i32, (R, per))
+    if level > 0:
+        depth = bp_parent.shape[0] if bp_parent is not None else 0
+        if depth < level:
+            raise ValueError(f"bp_parent holds {depth} steps, level is {level}")
+        bp = _need(bp_parent, "bp_parent", i32, (depth, R, B))
+        for t, name in ((k_beam, "k_beam"), (v_beam, "v_beam")):
+            if t is None or t.shape[0] < level:
+                raise ValueError(f"{name} holds fewer than {level} levels")
+        kb = _need(k_beam, "k_beam", torch.bfloat16, (k_beam.shape[0], rows, Hkv, D))
+        vb = _need(v_beam, "v_beam", torch.bfloat16, (v_beam.shape[0], rows, Hkv, D))
+    # Axes of one element: their stride means nothing, the packed one serves.
+    token = k_cache.stride(1) if page_size > 1 else Hkv * D
+    page = k_cache.stride(0) if n_pages > 1 else max(page_size * token, Hkv * D)
+    args = (_heads(q, "q", 1), q.stride(0) if rows > 1 else H * D, _heads(k_cache, "k_cache", 2, D),
+            _heads(v_cache, "v_cache", 2, D), page, token, n_pages, page_size, table, per,
+            _need(cache_len, "cache_len", i32, (R,)), int(level), bp, kb, vb, R, B, H, Hkv, D,
+            D ** -0.5 if scale is None else float(scale), _heads(out, "out", 1, D),
+            out.stride(0) if rows > 1 else H * D, _need(workspace, "workspace", workspace.dtype),
+            workspace.numel() * workspace.element_size())
+    _same_device(q, k_cache, v_cache, cache_len, out, workspace, page_table)
+    if level > 0:
+        _same_device(q, k_beam, v_beam, bp_parent)
+    _run_on(q, stream, load().beam_attention, *args)
 
 
 def sidbeam_get_device_status(workspace, stream=None) -> int:

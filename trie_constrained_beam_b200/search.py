@@ -12,6 +12,45 @@ import torch
 from . import native
 
 
+class LmheadFp8:
+    """One level's lm_head in 8 bits with the norm before it: the weight laid out
+    once (``lmhead_quantize_fp8``) and the row buffers of up to ``max_rows`` rows.
+
+    w_sid bf16 [V, d], norm_weight bf16 [d]; logits in ``dtype`` (bf16 or f32).
+    The buffers are rewritten by every call: one stream at a time.
+    """
+
+    def __init__(self, w_sid, norm_weight, max_rows: int, eps: float = 1e-6,
+                 dtype=torch.bfloat16, stream=None):
+        V, d = w_sid.shape
+        dev = w_sid.device
+        nb = -(-d // native.FP8_BLOCK)
+        self.V, self.d, self.eps, self.max_rows = V, d, float(eps), int(max_rows)
+        self.norm_weight = norm_weight
+        self.w_q = torch.empty((V, d), dtype=torch.float8_e4m3fn, device=dev)
+        self.w_scale = torch.empty((-(-V // native.FP8_BLOCK), nb), dtype=torch.float32, device=dev)
+        native.lmhead_quantize_fp8(w_sid, self.w_q, self.w_scale, stream=stream)
+        self.hidden_q = torch.empty((max_rows, d), dtype=torch.float8_e4m3fn, device=dev)
+        self.hidden_scale = torch.empty((max_rows, nb), dtype=torch.float32, device=dev)
+        # Rows of whole 16-byte units, as beam_step reads them.
+        self._logits = torch.empty((max_rows, -(-V // 8) * 8), dtype=dtype, device=dev)
+        self.workspace = torch.zeros(256, dtype=torch.uint8, device=dev)
+
+    def logits(self, x, residual=None, residual_out=None, stream=None):
+        """Logits [rows, V] of rows x (+ residual), bf16 [rows, d]; a view of this
+        object's buffer."""
+        rows = x.shape[0]
+        if rows > self.max_rows:
+            raise ValueError(f"{rows} rows, room for {self.max_rows}")
+        hq, hs = self.hidden_q[:rows], self.hidden_scale[:rows]
+        native.residual_rmsnorm_fp8(x, residual, self.norm_weight, self.eps, residual_out, hq, hs,
+                                    stream=stream)
+        out = self._logits[:rows, :self.V]
+        native.lmhead_logits_fp8(hq, hs, self.w_q, self.w_scale, out, self.workspace,
+                                 stream=stream)
+        return out
+
+
 class BeamSearch:
     def __init__(self, trie, R: int, n: int, V, depth: int = None, device="cuda",
                  skip_rows: bool = False, temperature: float = 0.0, seed: int = 0,
@@ -72,6 +111,22 @@ class BeamSearch:
                          self.scores[t], self.bp_parent[t], self.bp_code[t], self.nodes[t],
                          self.workspace, stream=stream, skip_rows=self.skip_rows,
                          out_width=self.widths)
+
+    def attention(self, t: int, q, k_cache, v_cache, cache_len, out, k_beam=None, v_beam=None,
+                  page_table=None, scale=None, stream=None):
+        """Attention of step t's rows (``beam_attention``): over their request's
+        prompt and, from step 1, the beams' own tokens chosen at steps 0 .. t-1,
+        found through this search's back-pointers. k_beam, v_beam bf16
+        [>= t, R*n, Hkv, D]: slice u holds the tokens that step u chose."""
+        native.beam_attention(q, k_cache, v_cache, cache_len, out, self.workspace,
+                              page_table=page_table, level=t, k_beam=k_beam, v_beam=v_beam,
+                              bp_parent=self.bp_parent, scale=scale, stream=stream)
+
+    def step_hidden(self, t: int, head: LmheadFp8, x, residual=None, residual_out=None,
+                    stream=None):
+        """Step t from hidden states bf16 [rows(t), d]: residual RMS norm and
+        lm_head in 8 bits (``head``), then the constrained step on its logits."""
+        self.step(t, head.logits(x, residual, residual_out, stream=stream), stream=stream)
 
     def skipped_rows(self, stream=None) -> int:
         """Rows left unread by row skipping since the last call."""
