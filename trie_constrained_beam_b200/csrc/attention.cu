@@ -14,6 +14,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 
 #include "internal.h"
@@ -37,41 +38,60 @@ struct AttnArgs {
   const int32_t* bp;
   const __nv_bfloat16 *kb, *vb;
   int R, B, H, Hkv;
-  float scale_log2;
+  float scale_log2;  // |scale| log2(e), never 0
+  uint32_t q_flip;   // sign bits of a bf16 pair: a negative scale negates q
   __nv_bfloat16* out;
   int64_t out_stride;
   uint32_t* status;
+  int G;              // H / Hkv
+  uint32_t g_magic;   // ceil(2^32 / G)
+  int pairs, units;
+  int split, split_log2;
+  int page_log2;      // of page_size (with a page table)
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -INFINITY;
 
 // ------------------------------------------------------------ shape of the work
-// A work item is (request, key/value head, two tiles of 128 rows): the rows of
-// the beams and of the H / Hkv heads that share the keys are one M axis, row
-// i = b * (H / Hkv) + head. Keys come in tiles of 128.
-//
-// One CTA runs two streams, each a chain S = Q K^T, softmax, O += P V with its
-// own S, P (in S's place) and O in TMEM, so that one stream's softmax runs under
-// the other's MMAs. With two row tiles the streams take one each and share every
-// key tile (loaded once). With one row tile both streams work on it, on every
-// other key tile, and their sums are joined at the end. Few items are split once
-// more along the keys over the CTAs of a cluster and joined through distributed
-// shared memory, always in the same order.
+// The rows of a request's beams and of the G = H / Hkv heads that share a key head
+// are one M axis, row i = b * G + head, in tiles of 128; keys come in tiles of 128.
+// A CTA runs two streams, each a chain S = Q K^T, softmax, O += P V with its own
+// S, P (in S's place) and O in TMEM, so that one stream's softmax runs under the
+// other's MMAs.
+//  kDual: a unit is two row tiles of a (request, key head); the streams take one
+//         each and share every key tile, which is loaded once for both.
+//  else:  a unit is one row tile; the streams take every other key tile, and the
+//         two (m, l, O) are joined at its end.
+// CTAs are persistent over units, with the rows' work in a warp group of its own:
+// while the streams run a unit, it scores the rows' ancestors and loads the next
+// unit's Q; while they run the next one, it joins, normalises and writes. Few
+// units are split over the keys among the CTAs of a cluster instead, and joined
+// through distributed shared memory in rank order.
 constexpr int kRows = 128;
 constexpr int kKeys = 128;
-constexpr int kThreads = 320;  // two softmax groups of 4 warps, TMA warp, MMA warp
-constexpr int kMaxSplit = 8;
+constexpr int kThreads = 512;  // softmax 0, softmax 1, rows, (TMA, MMA, -, -)
+constexpr int kMaxSplitLog2 = 3;
+constexpr uint16_t kNoSlot = 0xFFFFu;
 
-template <int D>
+template <int D, bool kDual>
 struct Plan {
-  static constexpr int kHalves = D / 64;             // 128-byte columns of a row
-  static constexpr int kTile = kKeys * D * 2;        // bytes of a K, V or Q tile
-  static constexpr int kHalf = kKeys * 128;          // bytes of one 64-column half
-  static constexpr int kSlots = D == 128 ? 5 : 8;    // ring of K and V tiles
-  static constexpr int kSmem = 2 * kTile + kSlots * kTile + 1024;
-  static constexpr int kPitch = D + 4;               // floats of a partial row: o, m, l
-  static_assert(2 * kRows * kPitch * 4 <= kSlots * kTile, "partials fit the ring");
+  static constexpr int kTiles = kDual ? 2 : 1;             // row tiles of a unit
+  static constexpr int kTile = kKeys * D * 2;              // bytes of a K, V or Q tile
+  static constexpr int kHalf = kKeys * 128;                // bytes of 64 of its columns
+  static constexpr int kSlots = D == 128 ? (kDual ? 4 : 5) : 8;  // ring of K and V tiles
+  static constexpr int kAhead = kDual ? 1 : 2;             // K tiles loaded before a V tile
+  static constexpr int kLevels = kDual ? 8 : SIDBEAM_MAX_DEPTH;
+  static constexpr int kPitch = 36;                        // floats of a staged row (32 used)
+  static constexpr int kStage = 4 * 32 * kPitch * 4;       // 32 columns of each warp's rows
+  static constexpr int kScores = kTiles * kRows * kLevels * 4;
+  static constexpr int kSlotTab = kTiles * kRows * kLevels * 2;
+  static constexpr int kMl = 2 * kRows * 8;
+  static constexpr int kRing = kTiles * kTile;             // offset of the ring (Q is first)
+  static constexpr int kAfter = kRing + kSlots * kTile;
+  static constexpr int kSmem = kAfter + kStage + kScores + kSlotTab + kMl + 1024;
+  static constexpr int kPart = D + 4;                      // floats of a partial row: o, m, l
+  static_assert(kTiles * kRows * kPart * 4 <= kAfter, "partial rows fit Q and the ring");
 };
 
 // Instruction descriptors (kind::f16, fp32 accumulator, bf16 operands, M = 128):
@@ -94,72 +114,111 @@ __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t addr, uint32_t half_by
          (static_cast<uint64_t>(2) << 61);
 }
 
-// The whole warp waits; one answer for all lanes.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort,
-                                          uint32_t* status) {
-  const bool ok = bounded_wait(bar, parity, abort, status, kStatusTimeout);
-  return __all_sync(0xFFFFFFFFu, ok);
-}
-
 struct Bars {
   uint64_t full[8], empty[8];
-  uint64_t q_ready[2], s_full[2], p_ready[2], o_full[2];
-  uint64_t v_clean, drain;
+  uint64_t q_full[2], q_empty[2];    // Q tile of a stream in place / multiplied
+  uint64_t s_full[2], p_ready[2];    // a step's scores / weights in TMEM
+  uint64_t ml_full[2], o_full[2];    // a unit's row maxima and sums / O complete
+  uint64_t o_empty[2];               // both have been read
+  uint64_t v_landed, v_clean;        // a ragged V tile is there / its tail is zero
+  uint64_t drain;
   uint32_t tmem;
   int abort;
 };
 
-// Position in the load order of key tile i's K and V (n tiles, K tiles loaded
-// `ahead` of the V tiles): K_0 .. K_{ahead-1}, then V_i, K_{i+ahead} in turn.
-__device__ __forceinline__ int pos_k(int i, int ahead) { return i + max(0, i - ahead + 1); }
-__device__ __forceinline__ int pos_v(int i, int ahead, int n) { return i + min(n, i + ahead); }
-
-// Element range 8 bf16 of a 16-byte unit.
-__device__ __forceinline__ void bf16x8(const uint4& u, float (&f)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+// 8 bf16 of a 16-byte word.
+__device__ __forceinline__ void bf16x4(const uint2& u, float (&f)[4]) {
+  f[0] = __uint_as_float(u.x << 16);
+  f[1] = __uint_as_float(u.x & 0xFFFF0000u);
+  f[2] = __uint_as_float(u.y << 16);
+  f[3] = __uint_as_float(u.y & 0xFFFF0000u);
 }
 
 // Byte offset of 16-byte unit c (0 .. D/8 - 1) of row `row` in a swizzled tile.
-template <int D>
 __device__ __forceinline__ uint32_t unit_at(int row, int c) {
-  return static_cast<uint32_t>((c >> 3) * Plan<D>::kHalf + row * 128 + (((c ^ row) & 7) << 4));
+  return static_cast<uint32_t>((c >> 3) * (kKeys * 128) + row * 128 + (((c ^ row) & 7) << 4));
 }
 
-template <int D>
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+}
+
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// One unit as every role sees it.
+struct Unit {
+  int r, g, row0, rows;  // request, key head, first row, valid rows (of all its tiles)
+  int t0, n, len;        // first key tile, key tiles, tokens of the request
+  int ragged;            // keys in the last tile if it is this CTA's and not full, else 0
+};
+
+template <bool kDual>
+__device__ __forceinline__ Unit unit_of(const AttnArgs& a, int w, int rank) {
+  Unit u;
+  const unsigned rg = static_cast<unsigned>(w) / static_cast<unsigned>(a.pairs);
+  const int pair = w - static_cast<int>(rg) * a.pairs;
+  u.r = static_cast<int>(rg / static_cast<unsigned>(a.Hkv));
+  u.g = static_cast<int>(rg) - u.r * a.Hkv;
+  constexpr int kUnitRows = kDual ? 2 * kRows : kRows;
+  u.row0 = pair * kUnitRows;
+  u.rows = min(kUnitRows, a.B * a.G - u.row0);
+  const int cap = a.table ? a.table_stride << a.page_log2 : a.page_size;
+  u.len = max(0, min(a.len[u.r], cap));
+  const int tiles = (u.len + kKeys - 1) / kKeys;  // < 2^24
+  u.t0 = (tiles * rank) >> a.split_log2;
+  const int t1 = (tiles * (rank + 1)) >> a.split_log2;
+  u.n = t1 - u.t0;
+  u.ragged = u.n > 0 && t1 == tiles ? u.len & (kKeys - 1) : 0;
+  return u;
+}
+
+// Steps of stream s (key tiles it works on) and the key tile of its step j.
+template <bool kDual>
+__device__ __forceinline__ int steps_of(const Unit& u, int s) {
+  return kDual ? (s == 0 || u.rows > kRows ? u.n : 0) : (u.n + 1 - s) >> 1;
+}
+template <bool kDual>
+__device__ __forceinline__ int tile_of(int s, int j) {
+  return kDual ? j : 2 * j + s;
+}
+
+// Positions in the load order of the T-th key tile's K and V, counted over all of
+// a CTA's units: K_0 .. K_{ahead-1}, then V_T, K_{T+ahead} in turn. (The positions
+// of K tiles past the last one stay unused; nothing follows in their slots.)
+__device__ __forceinline__ int pos_k(int t, int ahead) { return t < ahead ? t : 2 * t - ahead + 1; }
+__device__ __forceinline__ int pos_v(int t, int ahead) { return 2 * t + ahead; }
+
+template <int D, bool kDual>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap map_k,
-                     const __grid_constant__ CUtensorMap map_v, const AttnArgs a, int pairs,
-                     int split) {
-  using P = Plan<D>;
+                     const __grid_constant__ CUtensorMap map_v,
+                     const __grid_constant__ AttnArgs a) {
+  using P = Plan<D, kDual>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t* ring = smem + 2 * P::kTile;
+  uint8_t* ring = smem + P::kRing;
+  float* stage = reinterpret_cast<float*>(smem + P::kAfter);
+  float* scores = stage + P::kStage / 4;                        // [tiles][128][kLevels]
+  uint16_t* slots = reinterpret_cast<uint16_t*>(scores + P::kScores / 4);
+  float2* ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(slots) + P::kSlotTab);
   __shared__ Bars bar;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int rank = split > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int r = static_cast<int>(blockIdx.x) / (pairs * split), g = blockIdx.y;
-  const int G = a.H / a.Hkv;
-  const int row0 = (static_cast<int>(blockIdx.x) / split - r * pairs) * 2 * kRows;
-  const int rows = min(2 * kRows, a.B * G - row0);  // valid rows of both tiles
-  const bool dual = rows > kRows;
-
-  int64_t cap = a.table ? static_cast<int64_t>(a.table_stride) * a.page_size : a.page_size;
-  const int len_in = a.len[r];
-  const int len = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(len_in), cap)));
-  const int tiles = (len + kKeys - 1) / kKeys;
-  const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * rank / split);
-  const int n = static_cast<int>(static_cast<int64_t>(tiles) * (rank + 1) / split) - t0;
-  const int ahead = dual ? 1 : 2;
-  // Keys of the request's last tile if it is ragged and this CTA's, else 0.
-  const int ragged = (t0 + n == tiles) && n > 0 ? len & (kKeys - 1) : 0;
+  const int rank = a.split > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int first_unit = static_cast<int>(blockIdx.x) / a.split;
+  const int stride = a.split > 1 ? a.units : static_cast<int>(gridDim.x);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 8; ++s) {
@@ -167,453 +226,721 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar.empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
-      const int tile_rows = dual && s ? rows - kRows : min(rows, kRows);
-      const int active = (tile_rows + 31) / 32;
-      mbar_init(&bar.q_ready[s], active);
+      mbar_init(&bar.q_full[s], 4);
+      mbar_init(&bar.q_empty[s], 1);
       mbar_init(&bar.s_full[s], 1);
-      mbar_init(&bar.p_ready[s], active);
+      mbar_init(&bar.p_ready[s], 4);
+      mbar_init(&bar.ml_full[s], 4);
       mbar_init(&bar.o_full[s], 1);
+      mbar_init(&bar.o_empty[s], 4);
     }
+    mbar_init(&bar.v_landed, 1);
     mbar_init(&bar.v_clean, 1);
     mbar_init(&bar.drain, 1);
     bar.abort = 0;
-    if (len != len_in) atomicOr(a.status, kStatusBadCache);
     fence_mbar_init();
   }
-  if (warp == 9) tmem_alloc(&bar.tmem, 512);
+  if (warp == 13) tmem_alloc(&bar.tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bar.tmem;
+  const int quarter = warp & 3;
+  const uint32_t quad = static_cast<uint32_t>(quarter * 32) << 16;  // a warp's TMEM lanes
 
-  if (warp == 8) {
-    // ---------------------------------------------------------- loads
-    const int box = a.table ? min(a.page_size, kKeys) : kKeys;  // tokens of one copy
-    const int boxes = kKeys / box;
-    const int my_box = lane & (boxes - 1), my_half = lane / boxes;
-    const bool mine = my_half < P::kHalves;
-    if (lane == 0) {
-      prefetch_map(&map_k);
-      prefetch_map(&map_v);
-    }
-    const int loads = 2 * n;
-    int page_of = -1, page = 0;  // this lane's page number in tile `page_of`
-    int pos = 0, ki = 0, vi = 0;
-    for (; pos < loads; ++pos) {
-      const bool is_k = ki < n && ki < vi + ahead;
-      const int tile = t0 + (is_k ? ki : vi);
-      const int token = tile * kKeys + my_box * box;
-      const bool issue = mine && token < len;
-      if (a.table && issue && page_of != tile) {
-        page = a.table[static_cast<int64_t>(r) * a.table_stride + token / a.page_size];
-        if (page < 0 || page >= a.n_pages) {
-          atomicOr(a.status, kStatusBadCache);
-          page = a.n_pages;  // outside the tensor: the copy writes zeros
-        }
-        page_of = tile;
+  // Registers: 512 threads start with 128 each; 168 + 168 + 120 + 56 = 4 * 128.
+  if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 12) {
+      // -------------------------------------------------------- loads
+      const int box = a.table ? min(a.page_size, kKeys) : kKeys;  // tokens of one copy
+      const int boxes = kKeys / box;
+      const int my_box = lane & (boxes - 1), my_half = lane / boxes;
+      const bool mine = my_half < D / 64;
+      if (lane == 0) {
+        prefetch_map(&map_k);
+        prefetch_map(&map_v);
       }
-      const int s = pos % P::kSlots;
-      if (pos >= P::kSlots &&
-          !warp_wait(&bar.empty[s], ((pos / P::kSlots) - 1) & 1u, &bar.abort, a.status))
-        break;
-      const int count = min(boxes, (len - tile * kKeys + box - 1) / box);
-      if (lane == 0) mbar_arrive_expect_tx(&bar.full[s], count * P::kHalves * box * 128);
-      __syncwarp();
-      if (issue)
-        tma_load_4d(smem_addr(ring + s * P::kTile + my_half * P::kHalf + my_box * box * 128),
-                    is_k ? &map_k : &map_v, my_half * 64, g, a.table ? token & (a.page_size - 1) : token,
-                    a.table ? page : r, &bar.full[s]);
-      __syncwarp();
-      if (is_k) ++ki; else ++vi;
-    }
-    if (ragged && pos == loads) {
-      // The last V tile: rows past the end may hold anything, and 0 * NaN is
-      // not 0, so they are cleared once the copy has landed.
-      const int p = pos_v(n - 1, ahead, n), s = p % P::kSlots;
-      warp_wait(&bar.full[s], (p / P::kSlots) & 1u, &bar.abort, a.status);
-      constexpr int kUnits = D / 8;
-      for (int e = ragged * kUnits + lane; e < kKeys * kUnits; e += 32)
-        *reinterpret_cast<uint4*>(ring + s * P::kTile + unit_at<D>(e / kUnits, e % kUnits)) =
-            make_uint4(0u, 0u, 0u, 0u);
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.v_clean);
-    }
-    if (lane == 0)
-      for (int j = max(0, pos - P::kSlots); j < pos; ++j)
-        drain_wait(&bar.full[j % P::kSlots], (j / P::kSlots) & 1u);
-    __syncwarp();
-  } else if (warp == 9) {
-    // ---------------------------------------------------------- MMA issue
-    if (lane == 0 && n > 0) {
-      auto wait = [&](uint64_t* b, uint32_t parity) {
-        const bool ok = bounded_wait(b, parity, &bar.abort, a.status, kStatusTimeout);
-        tc_fence_after();
-        return ok;
+      // Two cursors over the same sequence of (unit, key tile).
+      struct Cursor {
+        int w, i, t;  // next unit index, tile of the unit, tiles loaded
+        Unit u;
       };
-      auto wait_load = [&](int pos) {
-        return wait(&bar.full[pos % P::kSlots], (pos / P::kSlots) & 1u);
-      };
-      auto free_load = [&](int pos) { umma_commit(&bar.empty[pos % P::kSlots]); };
-      auto qk = [&](int s, int i) {
-        const uint32_t qa = smem_addr(smem + (dual ? s : 0) * P::kTile);
-        const uint32_t ka = smem_addr(ring + (pos_k(i, ahead) % P::kSlots) * P::kTile);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * P::kHalf + (kk & 3) * 32;
-          umma_f16(tmem + s * kKeys, smem_desc(qa + off), smem_desc(ka + off), kIdescQK,
-                   kk > 0 ? 1u : 0u);
+      auto advance = [&](Cursor& c) {  // to the next tile; false past the last
+        ++c.i;
+        while (c.i >= c.u.n) {
+          c.w += stride;
+          if (c.w >= a.units) return false;
+          c.u = unit_of<kDual>(a, c.w, rank);
+          if (lane == 0 && c.u.len != a.len[c.u.r]) atomicOr(a.status, kStatusBadCache);
+          c.i = 0;
         }
-        umma_commit(&bar.s_full[s]);
+        return true;
       };
-      auto pv = [&](int s, int i, bool accumulate) {
-        const uint32_t va = smem_addr(ring + (pos_v(i, ahead, n) % P::kSlots) * P::kTile);
-#pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-          umma_f16_ts(tmem + 256 + s * 128, tmem + s * kKeys + kk * 8,
-                      smem_desc_mn(va + kk * 2048, P::kHalf), idesc_pv(D),
-                      kk > 0 || accumulate ? 1u : 0u);
-      };
-      const bool path = a.level > 0 && rank == 0;
-      bool ok = wait(&bar.q_ready[0], 0u) && (!dual || wait(&bar.q_ready[1], 0u));
-      if (dual) {
-        ok = ok && wait_load(pos_k(0, ahead));
-        if (ok) {
-          qk(0, 0);
-          qk(1, 0);
-          free_load(pos_k(0, ahead));
+      Cursor ck{first_unit - stride, 0, 0, {}}, cv;
+      ck.u.n = 0;
+      bool more_k = advance(ck);
+      cv = ck;
+      bool more_v = more_k;
+      int top = 0;  // positions issued
+      bool ok = true;
+#pragma unroll 1
+      while (ok && (more_k || more_v)) {
+        const bool is_k = more_k && ck.t < cv.t + P::kAhead;
+        const Cursor& c = is_k ? ck : cv;
+        const int pos = is_k ? pos_k(ck.t, P::kAhead) : pos_v(cv.t, P::kAhead);
+        const int tile = c.u.t0 + c.i;
+        const int token = tile * kKeys + my_box * box;
+        const bool issue = mine && token < c.u.len;
+        int page = c.u.r, at = token;
+        if (a.table) {
+          at = token & (a.page_size - 1);
+          if (issue) {
+            page = a.table[static_cast<int64_t>(c.u.r) * a.table_stride + (token >> a.page_log2)];
+            if (page < 0 || page >= a.n_pages) {
+              atomicOr(a.status, kStatusBadCache);
+              page = a.n_pages;  // outside the tensor: the copy writes zeros
+            }
+          }
         }
-        for (int i = 0; ok && i < n; ++i) {
-          for (int s = 0; ok && s < 2; ++s) {
-            ok = wait(&bar.p_ready[s], i & 1u);
-            if (ok && s == 0) ok = wait_load(pos_v(i, ahead, n));
-            if (ok && s == 0 && i == n - 1 && ragged) ok = wait(&bar.v_clean, 0u);
-            if (!ok) break;
-            pv(s, i, path || i > 0);
-            if (i + 1 < n) {
-              if (s == 0) ok = wait_load(pos_k(i + 1, ahead));
-              if (ok) qk(s, i + 1);
-            } else {
+        const int s = pos % P::kSlots;
+        if (pos >= P::kSlots &&
+            !warp_wait(&bar.empty[s], (pos / P::kSlots) - 1, &bar.abort, a.status)) {
+          ok = false;
+          break;
+        }
+        const int count = min(boxes, (c.u.len - tile * kKeys + box - 1) / box);
+        if (lane == 0) mbar_arrive_expect_tx(&bar.full[s], count * (D / 64) * box * 128);
+        __syncwarp();
+        if (issue)
+          tma_load_4d(smem_addr(ring + s * P::kTile + my_half * P::kHalf + my_box * box * 128),
+                      is_k ? &map_k : &map_v, my_half * 64, c.u.g, at, page, &bar.full[s]);
+        __syncwarp();
+        top = pos + 1;
+        if (is_k) {
+          ++ck.t;
+          more_k = advance(ck);
+        } else {
+          ++cv.t;
+          more_v = advance(cv);
+        }
+      }
+      // Copies in flight land before the CTA goes away (normally all have).
+#pragma unroll 1
+      for (int p = max(0, top - P::kSlots); p < top; ++p) {
+        // Position p was issued unless it is that of a K tile past the last one.
+        const bool v_pos = p >= P::kAhead && ((p - P::kAhead) & 1) == 0;
+        const int t = v_pos ? (p - P::kAhead) / 2
+                            : (p < P::kAhead ? p : (p + P::kAhead - 1) / 2);
+        if (v_pos ? t < cv.t : t < ck.t)
+          drain_wait(&bar.full[p % P::kSlots], (p / P::kSlots) & 1u);
+      }
+      __syncwarp();
+    } else if (warp == 13) {
+      // -------------------------------------------------------- MMA issue
+      if (elect_one()) {
+        bool ok = true;
+        auto wait = [&](uint64_t* b, int phase) {
+          ok = ok && lane_wait(b, static_cast<uint32_t>(phase), &bar.abort, a.status);
+        };
+        auto wait_load = [&](int pos) { wait(&bar.full[pos % P::kSlots], pos / P::kSlots); };
+        auto free_load = [&](int pos) { umma_commit(&bar.empty[pos % P::kSlots]); };
+        // One unit's place in the sequence: its key tiles follow `base` others.
+        struct Place {
+          Unit u;
+          int base, steps0, steps1, products;
+        };
+        int w = first_unit, tiles = 0;
+        auto next = [&](Place& p) {  // the next unit with key tiles
+          for (; w < a.units; w += stride) {
+            p.u = unit_of<kDual>(a, w, rank);
+            if (p.u.n > 0) {
+              w += stride;
+              p.base = tiles;
+              tiles += p.u.n;
+              p.steps0 = steps_of<kDual>(p.u, 0);
+              p.steps1 = steps_of<kDual>(p.u, 1);
+              p.products = 0;
+              return true;
+            }
+          }
+          p.steps0 = p.steps1 = 0;
+          return false;
+        };
+        int done0 = 0, done1 = 0;    // units behind, of each stream
+        int count0 = 0, count1 = 0;  // steps behind, of each stream
+        // S of step j of stream s: Q K^T.
+        auto product = [&](Place& p, int s, int j) {
+          const int pos = pos_k(p.base + tile_of<kDual>(s, j), P::kAhead);
+          if (j == 0) wait(&bar.q_full[kDual ? s : 0], kDual && s ? done1 : done0);
+          wait_load(pos);
+          if (!ok) return;
+          tc_fence_after();
+          const uint64_t q = smem_desc(smem_addr(smem + (kDual ? s : 0) * P::kTile));
+          const uint64_t k = smem_desc(smem_addr(ring + (pos % P::kSlots) * P::kTile));
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * P::kHalf + (kk & 3) * 32) >> 4;
+            umma_f16(tmem + s * kKeys, q + off, k + off, kIdescQK, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(&bar.s_full[s]);
+          ++p.products;
+          if (kDual ? j + 1 == p.steps0 : p.products == p.u.n)
+            umma_commit(&bar.q_empty[kDual ? s : 0]);
+          if (!kDual || s == 1 || p.steps1 == 0) free_load(pos);
+        };
+        Place p, nx;
+        bool have = next(p);
+#pragma unroll 1
+        for (int s = 0; have && s < 2; ++s)
+          if ((s ? p.steps1 : p.steps0) > 0) product(p, s, 0);
+        int cleaned = 0;
+        while (ok && have) {
+          const bool more = next(nx);
+#pragma unroll 1
+          for (int e = 0; ok && e < 2 * p.steps0; ++e) {
+            const int j = e >> 1, s = e & 1;
+            const int steps = s ? p.steps1 : p.steps0;
+            if (j < steps) {
+              const int i = tile_of<kDual>(s, j);
+              const int pos = pos_v(p.base + i, P::kAhead);
+              const bool clean = p.u.ragged && i == p.u.n - 1 && (!kDual || s == 0);
+              if (clean) {
+                wait_load(pos);
+                mbar_arrive(&bar.v_landed);
+              }
+              wait(&bar.p_ready[s], s ? count1 : count0);
+              if (s) ++count1; else ++count0;
+              wait_load(pos);
+              if (clean) wait(&bar.v_clean, cleaned++);
+              const int done = s ? done1 : done0;
+              if (j == 0 && done > 0) wait(&bar.o_empty[s], done - 1);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t v = smem_desc_mn(smem_addr(ring + (pos % P::kSlots) * P::kTile), P::kHalf);
+#pragma unroll
+              for (int kk = 0; kk < kKeys / 16; ++kk)
+                umma_f16_ts(tmem + 256 + s * 128, tmem + s * kKeys + kk * 8, v + kk * (2048 >> 4),
+                            idesc_pv(D), kk > 0 || j > 0 ? 1u : 0u);
+              if (!kDual || s == 1 || p.steps1 == 0) free_load(pos);
+            }
+            // The stream's next product: of this unit, or (at its last step, or
+            // at once where it has none) the first of the next unit.
+            Place* to = nullptr;
+            int to_j = 0;
+            if (j + 1 < steps) {
+              to = &p;
+              to_j = j + 1;
+            } else if (j + 1 == steps) {
               umma_commit(&bar.o_full[s]);
+              if (s) ++done1; else ++done0;
+            }
+            if (kDual && !to && j + 1 == p.steps0 && (s ? nx.steps1 : nx.steps0) > 0) to = &nx;
+            if (to) product(*to, s, to_j);
+          }
+          if (!kDual)
+#pragma unroll 1
+            for (int s = 0; ok && s < 2; ++s)
+              if ((s ? nx.steps1 : nx.steps0) > 0) product(nx, s, 0);
+          p = nx;
+          have = more;
+        }
+        umma_commit(&bar.drain);
+        drain_wait(&bar.drain, 0u);
+      }
+      __syncwarp();
+    } else if (warp == 14) {
+      // -------------------------------------------------------- tails of V
+      // Rows of V past a request's end may hold anything, and 0 * NaN is not 0:
+      // they are cleared between the copy and the product.
+      int tiles = 0, cleaned = 0;
+      for (int w = first_unit; w < a.units; w += stride) {
+        const Unit u = unit_of<kDual>(a, w, rank);
+        tiles += u.n;
+        if (!u.ragged) continue;
+        if (!warp_wait(&bar.v_landed, cleaned++, &bar.abort, a.status)) break;
+        uint8_t* vt = ring + (pos_v(tiles - 1, P::kAhead) % P::kSlots) * P::kTile;
+        constexpr int kUnits = D / 8;
+#pragma unroll 4
+        for (int e = u.ragged * kUnits + lane; e < kKeys * kUnits; e += 32)
+          *reinterpret_cast<uint4*>(vt + unit_at(e / kUnits, e % kUnits)) =
+              make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.v_clean);
+      }
+    }
+  } else if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    // ---------------------------------------------------------- softmax
+    const int s = warp >> 2;
+    const uint32_t t_s = tmem + s * kKeys + quad, t_o = tmem + 256 + s * 128 + quad;
+    const float sc = a.scale_log2;
+    int count = 0, done = 0;
+    bool ok = true;
+    for (int w = first_unit; ok && w < a.units; w += stride) {
+      const Unit u = unit_of<kDual>(a, w, rank);
+      const int steps = steps_of<kDual>(u, s);
+      if (steps == 0) continue;
+      const int tile_rows = kDual && s == 1 ? u.rows - kRows : min(u.rows, kRows);
+      const bool active = quarter * 32 < tile_rows;
+      float m = kNegInf, l = 0.f;
+      for (int j = 0; j < steps; ++j, ++count) {
+        if (!warp_wait(&bar.s_full[s], count, &bar.abort, a.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (active) {
+          float x[kKeys];
+#pragma unroll
+          for (int c = 0; c < kKeys; c += 32)
+            tmem_ld32_async(t_s + c, reinterpret_cast<uint32_t*>(x) + c);
+          tmem_wait_ld();
+          if (u.ragged && tile_of<kDual>(s, j) == u.n - 1) {
+#pragma unroll
+            for (int e = 0; e < kKeys; ++e)
+              if (e >= u.ragged) x[e] = kNegInf;
+          }
+          float t4[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) t4[e] = fmaxf(x[e], x[e + 4]);
+#pragma unroll
+          for (int e = 8; e < kKeys; e += 8) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) t4[k] = fmaxf(fmaxf(t4[k], x[e + k]), x[e + 4 + k]);
+          }
+          const float t = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * sc;
+          // The reference m moves only when a row's maximum passes it by 2^8:
+          // smaller growth keeps the weights below 2^8 and spares the pass over O.
+          if (j == 0) {
+            m = t;
+          } else if (const bool grow = t > m + 8.f; __any_sync(0xFFFFFFFFu, grow)) {
+            // A row that need not move keeps its reference, so that no row's
+            // result depends on its neighbours.
+            const float f = grow ? ex2_approx(m - t) : 1.f;
+            l *= f;
+            m = grow ? t : m;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(t_o + c, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st16(t_o + c, o);
             }
           }
-          if (!ok) break;
-          free_load(pos_v(i, ahead, n));
-          if (i + 1 < n) free_load(pos_k(i + 1, ahead));
+          const float mref = m > kNegInf ? m : 0.f;
+          const uint64_t sc2 = pack_f32x2(sc, sc), m2 = pack_f32x2(-mref, -mref);
+          uint64_t l2[2] = {pack_f32x2(l, 0.f), pack_f32x2(0.f, 0.f)};
+#pragma unroll
+          for (int c = 0; c < kKeys; c += 32) {
+            uint32_t p[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float p0, p1;
+              unpack_f32x2(fma_f32x2(pack_f32x2(x[c + e], x[c + e + 1]), sc2, m2), p0, p1);
+              p0 = ex2_approx(p0);
+              p1 = ex2_approx(p1);
+              l2[(e >> 1) & 1] = add_f32x2(l2[(e >> 1) & 1], pack_f32x2(p0, p1));
+              p[e >> 1] = bf16x2(p0, p1);
+            }
+            tmem_st16(t_s + (c >> 1), p);
+          }
+          float la, lb;
+          unpack_f32x2(add_f32x2(l2[0], l2[1]), la, lb);
+          l = la + lb;
+          tmem_wait_st();
         }
-      } else {
-        for (int s = 0; ok && s < min(2, n); ++s) {
-          ok = wait_load(pos_k(s, ahead));
-          if (!ok) break;
-          qk(s, s);
-          free_load(pos_k(s, ahead));
-        }
-        for (int i = 0; ok && i < n; ++i) {
-          const int s = i & 1;
-          ok = wait(&bar.p_ready[s], (i >> 1) & 1u) && wait_load(pos_v(i, ahead, n)) &&
-               (!(ragged && i == n - 1) || wait(&bar.v_clean, 0u));
-          if (!ok) break;
-          pv(s, i, (path && s == 0) || i > 1);
-          free_load(pos_v(i, ahead, n));
-          if (i + 2 < n) {
-            ok = wait_load(pos_k(i + 2, ahead));
-            if (!ok) break;
-            qk(s, i + 2);
-            free_load(pos_k(i + 2, ahead));
-          } else {
-            umma_commit(&bar.o_full[s]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.p_ready[s]);
+      }
+      if (!ok) break;
+      if (done > 0 && !warp_wait(&bar.o_empty[s], done - 1, &bar.abort, a.status)) break;
+      ml[s * kRows + quarter * 32 + lane] = make_float2(m, l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.ml_full[s]);
+      ++done;
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+    // ---------------------------------------------------------- rows
+    // A warp keeps to the 32 rows of its TMEM lanes (of each tile) throughout, so
+    // its pieces of Q, scores and staging need no barrier beyond the warp.
+    float* my_stage = stage + quarter * 32 * P::kPitch;
+    const int my0 = quarter * 32;  // first of the warp's rows in a tile
+    int done0 = 0, done1 = 0;      // units behind, of each stream
+    bool ok = true;
+    auto beam_of = [&](int i) { return static_cast<int>(__umulhi(static_cast<uint32_t>(i), a.g_magic)); };
+    // (2^32 / 1 does not fit the magic factor.)
+    auto split_row = [&](int i, int& b, int& h) {
+      b = a.G == 1 ? i : beam_of(i);
+      h = i - b * a.G;
+    };
+    auto rows_of = [&](const Unit& u, int tile) { return min(kRows, u.rows - tile * kRows); };
+
+    // Q of unit u into its tiles, behind the last product with the ones before.
+    // (`more0`, `more1`: the unit before, not yet counted, used the stream.)
+    auto load_q = [&](const Unit& u, int more0, int more1) {
+#pragma unroll 1
+      for (int t = 0; t < P::kTiles; ++t) {
+        const int users = t ? done1 + more1 : done0 + more0;
+        if (users > 0 && !warp_wait(&bar.q_empty[t], users - 1, &bar.abort, a.status)) ok = false;
+      }
+      if (!ok) return;
+      constexpr int kUnits = D / 8, kPer = 32 / kUnits;
+      const int c = lane % kUnits;
+#pragma unroll 1
+      for (int t = 0; t < P::kTiles; ++t) {
+        uint8_t* qt = smem + t * P::kTile;
+        const int valid = rows_of(u, t);
+#pragma unroll 4
+        for (int j = 0; j < kUnits; ++j) {
+          const int lr = my0 + j * kPer + lane / kUnits;
+          if (lr < valid) {
+            int b, h;
+            split_row(u.row0 + t * kRows + lr, b, h);
+            cp_async16(qt + unit_at(lr, c), a.q + (static_cast<int64_t>(u.r) * a.B + b) * a.q_stride +
+                                                (u.g * a.G + h) * D + c * 8);
           }
         }
       }
-      umma_commit(&bar.drain);
-      drain_wait(&bar.drain, 0u);
-    }
-    __syncwarp();
-  }
-  // The softmax warps' state lives past this point: their rows' o, m and l.
-  const int s = warp >> 2;                         // stream of a softmax warp
-  const int quarter = warp & 3;                    // its TMEM lanes
-  const int tile_row = quarter * 32;               // first of its 32 rows in the tile
-  const int first = row0 + (dual && s == 1 ? kRows : 0);
-  const int tile_rows = dual && s == 1 ? rows - kRows : min(rows, kRows);
-  const bool active = warp < 8 && tile_row < tile_rows;
-  const int n_s = dual ? n : (n + 1 - s) / 2;      // key tiles of this stream
-  const bool init = a.level > 0 && rank == 0 && (dual || s == 0);
-  const uint32_t quad = static_cast<uint32_t>(tile_row) << 16;
-  const uint32_t t_s = tmem + s * kKeys + quad, t_o = tmem + 256 + s * 128 + quad;
-  float m = kNegInf, l = 0.f;
-  bool dead = false;
-  if (active) {
-    // ---------------------------------------------------------- Q, path
-    const int lrow = tile_row + lane;              // row of the tile
-    const int i_row = first + lrow;
-    const bool valid = lrow < tile_rows;
-    uint8_t* qt = smem + (dual ? s : 0) * P::kTile;
-    if (dual || s == 0) {
-      // Coalesced: D / 8 lanes read a row. A negative scale flips q's signs (the
-      // maximum below needs a factor >= 0).
-      constexpr int kUnits = D / 8, kPer = 32 / kUnits;
-      const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-      const int c = lane % kUnits;
-#pragma unroll 8
-      for (int j = 0; j < kUnits; ++j) {
-        const int lr = tile_row + j * kPer + lane / kUnits;
-        if (lr < tile_rows) {
-          const int i = first + lr, b = i / G, h = g * G + (i - b * G);
-          uint4 u = *reinterpret_cast<const uint4*>(
-              a.q + (static_cast<int64_t>(r) * a.B + b) * a.q_stride + h * D + c * 8);
-          u.x ^= flip;
-          u.y ^= flip;
-          u.z ^= flip;
-          u.w ^= flip;
-          *reinterpret_cast<uint4*>(qt + unit_at<D>(lr, c)) = u;
-        }
+      cp_async_wait();
+      __syncwarp();
+      if (a.q_flip) {
+        for (int t = 0; t < P::kTiles; ++t)
+#pragma unroll 1
+          for (int e = lane; e < 32 * kUnits; e += 32) {
+            uint4* q = reinterpret_cast<uint4*>(smem + t * P::kTile + unit_at(my0 + e / kUnits, e % kUnits));
+            *q = make_uint4(q->x ^ a.q_flip, q->y ^ a.q_flip, q->z ^ a.q_flip, q->w ^ a.q_flip);
+          }
       }
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.q_ready[s]);
-    }
-    const float sc = fabsf(a.scale_log2);
-    if (a.level > 0) {
-      int slot[SIDBEAM_MAX_DEPTH];
-      float x[SIDBEAM_MAX_DEPTH];
-      int at = valid ? i_row / G : -1;
-      for (int u = a.level - 1; u >= 0; --u) {
-        slot[u] = at;
+      for (int t = 0; t < P::kTiles; ++t)
+        if (steps_of<kDual>(u, t) > 0 && lane == 0) mbar_arrive(&bar.q_full[t]);
+    };
+
+    // Scores of the rows' ancestors, for the warp's rows of a tile: 16 rows by
+    // the (at most 16) beams they belong to, one level at a time, on the small
+    // tensor-core product; of the 16 x 8 block only a row's own beam is kept.
+    // The order of D inside the product is free as long as both sides share it,
+    // so each lane reads whole 16-byte words. Returns whether lane's row is dead.
+    auto score_path = [&](const Unit& u, int tile) {
+      const int valid = rows_of(u, tile) - my0;  // of this warp's rows
+      if (valid <= 0) return false;
+      uint16_t* tab = slots + (tile * kRows + my0) * P::kLevels;
+      float* xs = scores + (tile * kRows + my0) * P::kLevels;
+      const int i0 = u.row0 + tile * kRows + my0;
+      int b, h, at = -1;
+      if (lane < valid) {
+        split_row(i0 + lane, b, h);
+        at = b;
+      }
+#pragma unroll 1
+      for (int v = a.level - 1; v >= 0; --v) {
+        tab[lane * P::kLevels + v] = at < 0 ? kNoSlot : static_cast<uint16_t>(at);
         if (at >= 0) {
-          const int p = a.bp[(static_cast<int64_t>(u) * a.R + r) * a.B + at];
-          at = p < 0 ? -1 : (u > 0 && p >= a.B ? -1 : p);
+          const int p = a.bp[(static_cast<int64_t>(v) * a.R + u.r) * a.B + at];
+          at = p < 0 || (v > 0 && p >= a.B) ? -1 : p;
         }
       }
-      dead = at < 0;
-      if (init) {
-        const int64_t hd = static_cast<int64_t>(a.Hkv) * D;
-        if (!dead) {
-          for (int u = 0; u < a.level; ++u) {
-            const uint4* k = reinterpret_cast<const uint4*>(
-                a.kb + ((static_cast<int64_t>(u) * a.R + r) * a.B + slot[u]) * hd + g * D);
-            float z = 0.f;
+      __syncwarp();
+      const int c = lane & 3, n8 = lane >> 2;
+      constexpr int kWords = D / 32;  // 16-byte words of a lane's quarter of D
+      const uint8_t* qt = smem + tile * P::kTile;
+#pragma unroll 1
+      for (int rg = 0; rg < 32 && rg < valid; rg += 16) {
+        uint4 qa[kWords], qb[kWords];
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-              float kf[8], qf[8];
-              bf16x8(k[c], kf);
-              bf16x8(*reinterpret_cast<const uint4*>(qt + unit_at<D>(lrow, c)), qf);
+        for (int k = 0; k < kWords; ++k) {
+          qa[k] = *reinterpret_cast<const uint4*>(qt + unit_at(my0 + rg + n8, c * kWords + k));
+          qb[k] = *reinterpret_cast<const uint4*>(qt + unit_at(my0 + rg + n8 + 8, c * kWords + k));
+        }
+        int b0, b_lo, b_hi, b_end, hh;
+        split_row(i0 + rg, b0, hh);
+        split_row(i0 + rg + n8, b_lo, hh);
+        split_row(i0 + rg + n8 + 8, b_hi, hh);
+        split_row(i0 + min(rg + 15, valid - 1), b_end, hh);
+#pragma unroll 1
+        for (int n0 = 0; n0 <= b_end - b0; n0 += 8) {
+          // This lane's key: beam b0 + n0 + n8, through its first row in the group.
+          const int kb = b0 + n0 + n8;
+          const int krow = max(rg, kb * a.G - i0);
+#pragma unroll 1
+          for (int v = 0; v < a.level; ++v) {
+            const uint16_t slot = kb <= b_end ? tab[krow * P::kLevels + v] : kNoSlot;
+            uint4 kw[kWords];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) z = fmaf(kf[e], qf[e], z);
+            for (int k = 0; k < kWords; ++k) kw[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (slot != kNoSlot) {
+              const uint4* src = reinterpret_cast<const uint4*>(
+                  a.kb + (((static_cast<int64_t>(v) * a.R + u.r) * a.B + slot) * a.Hkv + u.g) * D +
+                  c * (D / 4));
+#pragma unroll
+              for (int k = 0; k < kWords; ++k) kw[k] = src[k];
             }
-            x[u] = z * sc;
-            m = fmaxf(m, x[u]);
-          }
-          for (int u = 0; u < a.level; ++u) {
-            x[u] = ex2_approx(x[u] - m);
-            l += x[u];
+            float z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < kWords; ++k) {
+              mma_16816(z, qa[k].x, qb[k].x, qa[k].y, qb[k].y, kw[k].x, kw[k].y);
+              mma_16816(z, qa[k].z, qb[k].z, qa[k].w, qb[k].w, kw[k].z, kw[k].w);
+            }
+            const int j_lo = b_lo - b0 - n0, j_hi = b_hi - b0 - n0;
+            if (j_lo >= 0 && j_lo < 8 && (j_lo >> 1) == c)
+              xs[(rg + n8) * P::kLevels + v] = (j_lo & 1 ? z[1] : z[0]) * a.scale_log2;
+            if (j_hi >= 0 && j_hi < 8 && (j_hi >> 1) == c)
+              xs[(rg + n8 + 8) * P::kLevels + v] = (j_hi & 1 ? z[3] : z[2]) * a.scale_log2;
           }
         }
-        for (int c0 = 0; c0 < D; c0 += 32) {
-          float o[32];
+      }
+      __syncwarp();
+      return at < 0;
+    };
+
+    // 64 columns of the warp's rows: the path's share, then out.
+    auto write_half = [&](const Unit& u, const float (&o)[64], int h0, int valid, bool path,
+                          float* part, const uint16_t* tab, const float* ws, int i0) {
+      const int c4 = (lane & 7) * 4, r4 = lane >> 3;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0.f;
-          if (!dead) {
-            for (int u = 0; u < a.level; ++u) {
-              const uint4* v = reinterpret_cast<const uint4*>(
-                  a.vb + ((static_cast<int64_t>(u) * a.R + r) * a.B + slot[u]) * hd + g * D + c0);
+      for (int c = 0; c < 64; c += 32) {
+        const int c0 = h0 + c;
+        // 32 columns through shared memory: from a row per lane to 8 lanes a row.
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                float vf[8];
-                bf16x8(v[c], vf);
+        for (int e = 0; e < 32; e += 4)
+          *reinterpret_cast<float4*>(my_stage + lane * P::kPitch + e) =
+              make_float4(o[c + e], o[c + e + 1], o[c + e + 2], o[c + e + 3]);
+        __syncwarp();
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+          if (q * 16 >= valid) break;
+          float4 y[4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[c * 8 + e] = fmaf(x[u], vf[e], o[c * 8 + e]);
+          for (int k = 0; k < 4; ++k)
+            y[k] = *reinterpret_cast<const float4*>(my_stage + (q * 16 + k * 4 + r4) * P::kPitch + c4);
+          if (path) {
+#pragma unroll 1
+            for (int v = 0; v < a.level; ++v) {
+              const __nv_bfloat16* src =
+                  a.vb + ((static_cast<int64_t>(v) * a.R + u.r) * a.B * a.Hkv + u.g) * D + c0 + c4;
+              uint2 vw[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint16_t slot = tab[(q * 16 + k * 4 + r4) * P::kLevels + v];
+                vw[k] = make_uint2(0u, 0u);
+                if (slot != kNoSlot)
+                  vw[k] = *reinterpret_cast<const uint2*>(src + static_cast<int64_t>(slot) * a.Hkv * D);
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float wt = ws[(q * 16 + k * 4 + r4) * P::kLevels + v];
+                float vf[4];
+                bf16x4(vw[k], vf);
+                if (wt > 0.f) {
+                  y[k].x = fmaf(wt, vf[0], y[k].x);
+                  y[k].y = fmaf(wt, vf[1], y[k].y);
+                  y[k].z = fmaf(wt, vf[2], y[k].z);
+                  y[k].w = fmaf(wt, vf[3], y[k].w);
+                }
               }
             }
           }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int lr = q * 16 + k * 4 + r4;
+            if (lr < valid) {
+              if (a.split > 1) {
+                *reinterpret_cast<float4*>(part + lr * P::kPart + c0 + c4) = y[k];
+              } else {
+                int b, h;
+                split_row(i0 + lr, b, h);
+                *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(u.r) * a.B + b) * a.out_stride +
+                                          (u.g * a.G + h) * D + c0 + c4) =
+                    make_uint2(bf16x2(y[k].x, y[k].y), bf16x2(y[k].z, y[k].w));
+              }
+            }
+          }
+        }
+        __syncwarp();
+      }
+    };
+
+    // Joins the streams and the path of the warp's rows of a tile, and writes
+    // them: bf16 rows, or (split keys) partial rows in fp32.
+    auto finish = [&](const Unit& u, int tile, bool dead) {
+      const int valid = rows_of(u, tile) - my0;
+      const int s_end = kDual ? tile + 1 : 2;
+      const bool path = a.level > 0 && rank == 0;
+      float* xs = scores + (tile * kRows + my0 + lane) * P::kLevels;
+      float2 st_a = make_float2(kNegInf, 0.f), st_b = st_a;
+#pragma unroll 1
+      for (int s = kDual ? tile : 0; s < s_end; ++s) {
+        if (steps_of<kDual>(u, s) == 0) continue;
+        const int done = s ? done1 : done0;
+        if (!warp_wait(&bar.ml_full[s], done, &bar.abort, a.status) ||
+            !warp_wait(&bar.o_full[s], done, &bar.abort, a.status)) {
+          ok = false;
+          return;
+        }
+        const float2 got = ml[s * kRows + my0 + lane];
+        if (kDual || s == 0) st_a = got; else st_b = got;
+      }
+      tc_fence_after();
+      float top = kNegInf, sum = 0.f, f0 = 0.f, f1 = 0.f;
+      if (valid > 0) {
+        // Weights: one reference for all sources of the row.
+        top = fmaxf(st_a.y > 0.f ? st_a.x : kNegInf, st_b.y > 0.f ? st_b.x : kNegInf);
+        if (path)
+#pragma unroll 1
+          for (int v = 0; v < a.level; ++v) top = fmaxf(top, xs[v]);
+        const float ref = top > kNegInf ? top : 0.f;
+        f0 = st_a.y > 0.f ? ex2_approx(st_a.x - ref) : 0.f;
+        f1 = st_b.y > 0.f ? ex2_approx(st_b.x - ref) : 0.f;
+        sum = f0 * st_a.y + f1 * st_b.y;
+        if (path)
+#pragma unroll 1
+          for (int v = 0; v < a.level; ++v) {
+            xs[v] = ex2_approx(xs[v] - ref);
+            sum += xs[v];
+          }
+        if (dead) {
+          sum = 0.f;
+          top = kNegInf;
+        }
+        const float inv = a.split > 1 ? (dead ? 0.f : 1.f) : (sum > 0.f ? 1.f / sum : 0.f);
+        f0 *= inv;
+        f1 *= inv;
+        if (path)
+#pragma unroll 1
+          for (int v = 0; v < a.level; ++v) xs[v] = dead ? 0.f : xs[v] * inv;
+      }
+      float* part = reinterpret_cast<float*>(smem) + (tile * kRows + my0) * P::kPart;
+      if (a.split > 1 && valid > 0) {
+        part[lane * P::kPart + D] = top;
+        part[lane * P::kPart + D + 1] = sum;
+      }
+      const int sa = kDual ? tile : 0;
+      const bool has_a = steps_of<kDual>(u, sa) > 0, has_b = !kDual && steps_of<kDual>(u, 1) > 0;
+      const uint16_t* tab = slots + (tile * kRows + my0) * P::kLevels;
+      const float* ws = scores + (tile * kRows + my0) * P::kLevels;
+      const int i0 = u.row0 + tile * kRows + my0;
+#pragma unroll 1
+      for (int h0 = 0; h0 < D; h0 += 64) {
+        float o[64];
+#pragma unroll
+        for (int e = 0; e < 64; ++e) o[e] = 0.f;
+        if (valid > 0 && has_a) {
+          const uint32_t t_o = tmem + 256 + sa * 128 + quad + h0;
+          tmem_ld32_async(t_o, reinterpret_cast<uint32_t*>(o));
+          tmem_ld32_async(t_o + 32, reinterpret_cast<uint32_t*>(o) + 32);
+          tmem_wait_ld();
+          // A dead row's q may hold anything, its O then too.
+#pragma unroll
+          for (int e = 0; e < 64; ++e) o[e] = dead ? 0.f : o[e] * f0;
+        }
+        if (valid > 0 && has_b) {
+#pragma unroll
+          for (int c = 0; c < 64; c += 16) {
+            uint32_t v[16];
+            tmem_ld16(tmem + 256 + 128 + quad + h0 + c, v);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              o[c + e] = dead ? 0.f : fmaf(__uint_as_float(v[e]), f1, o[c + e]);
+          }
+        }
+        if (h0 + 64 == D) {  // O has been read
+          tc_fence_before();
           __syncwarp();
-          tmem_st32(t_o + c0, reinterpret_cast<const uint32_t*>(o));
+          for (int s = kDual ? tile : 0; s < s_end; ++s)
+            if (steps_of<kDual>(u, s) > 0) {
+              if (lane == 0) mbar_arrive(&bar.o_empty[s]);
+              if (s) ++done1; else ++done0;
+            }
         }
-        tmem_wait_st();
-        tc_fence_before();
+        if (valid > 0) write_half(u, o, h0, valid, path, part, tab, ws, i0);
       }
+    };
+
+    Unit u;
+    if (first_unit < a.units) {
+      u = unit_of<kDual>(a, first_unit, rank);
+      load_q(u, 0, 0);
     }
-    // ---------------------------------------------------------- softmax
-    bool started = init;
-    for (int j = 0; j < n_s; ++j) {
-      if (!warp_wait(&bar.s_full[s], j & 1u, &bar.abort, a.status)) break;
-      tc_fence_after();
-      float x[kKeys];
-#pragma unroll
-      for (int c = 0; c < kKeys; c += 32)
-        tmem_ld32_async(t_s + c, reinterpret_cast<uint32_t*>(x) + c);
-      tmem_wait_ld();
-      const bool cut = ragged && j == n_s - 1 && (dual || ((n - 1) & 1) == s);
-      if (cut) {
-#pragma unroll
-        for (int e = 0; e < kKeys; ++e)
-          if (e >= ragged) x[e] = kNegInf;
+    for (int w = first_unit; ok && w < a.units; w += stride) {
+      uint32_t dead = 0u;  // bit t: this lane's row of tile t
+      if (a.level > 0)
+#pragma unroll 1
+        for (int t = 0; t * kRows < u.rows; ++t)
+          if (score_path(u, t)) dead |= 1u << t;
+      // done[] still counts the units before this one: its Q is in use until its
+      // own products are done, which is what the next load waits for.
+      const int w2 = w + stride;
+      Unit nx = u;
+      if (w2 < a.units) {
+        nx = unit_of<kDual>(a, w2, rank);
+        load_q(nx, steps_of<kDual>(u, 0) > 0, steps_of<kDual>(u, 1) > 0);
       }
-      float t = x[0];
-#pragma unroll
-      for (int e = 1; e < kKeys; ++e) t = fmaxf(t, x[e]);
-      t *= sc;
-      // The reference m moves only when a row's maximum passes it by 2^8: smaller
-      // growth keeps the weights below 2^8 and spares the pass over O.
-      const bool grow = !started || t > m + 8.f;
-      if (__any_sync(0xFFFFFFFFu, grow)) {
-        const float mn = fmaxf(m, t);
-        if (started) {
-          const float f = m > kNegInf ? ex2_approx(m - mn) : 0.f;
-          l *= f;
-#pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(t_o + c, o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st32(t_o + c, o);
-          }
-        }
-        m = mn;
-        started = true;
+      if (ok && a.split > 1 && kDual) {
+        // Partial rows go where Q and the ring are: both streams end first.
+        for (int s = 0; s < 2; ++s)
+          if (steps_of<kDual>(u, s) > 0 &&
+              !warp_wait(&bar.o_full[s], s ? done1 : done0, &bar.abort, a.status))
+            ok = false;
       }
-      uint32_t p[kKeys / 2];
-      float l0 = 0.f, l1 = 0.f;
-      const float mref = m > kNegInf ? m : 0.f;
-#pragma unroll
-      for (int e = 0; e < kKeys; e += 2) {
-        float p0 = ex2_approx(fmaf(x[e], sc, -mref)), p1 = ex2_approx(fmaf(x[e + 1], sc, -mref));
-        if (cut) {
-          p0 = e < ragged ? p0 : 0.f;
-          p1 = e + 1 < ragged ? p1 : 0.f;
-        }
-        l0 += p0;
-        l1 += p1;
-        p[e / 2] = bf16x2(p0, p1);
-      }
-      l += l0 + l1;
-      tmem_st32(t_s, p);
-      tmem_st32(t_s + 32, p + 32);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.p_ready[s]);
+      if (a.split > 1) named_sync(1, 128);  // one unit only; every warp has read Q
+#pragma unroll 1
+      for (int t = 0; ok && t * kRows < u.rows; ++t) finish(u, t, (dead >> t & 1u) != 0u);
+      u = nx;
     }
-    if (n_s > 0) {
-      warp_wait(&bar.o_full[s], 0u, &bar.abort, a.status);
-      tc_fence_after();
-    }
-    if (dead) l = 0.f;
   }
-  const bool has_o = n_s > 0 || init;
-  if (dual && split == 1) {
-    // ---------------------------------------------------------- direct output
-    if (active) {
-      // The warp's own rows of the Q tile (its MMAs are done) take the rows'
-      // bf16 results and give them back in whole 128-byte lines.
-      uint8_t* qt = smem + s * P::kTile;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
-        if (has_o) {
-          tmem_ld32(t_o + c, o);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0u;
-        }
-        float f[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) f[e] = l > 0.f ? __uint_as_float(o[e]) * inv : 0.f;
-#pragma unroll
-        for (int e = 0; e < 32; e += 8)
-          *reinterpret_cast<uint4*>(qt + unit_at<D>(tile_row + lane, (c + e) / 8)) =
-              make_uint4(bf16x2(f[e], f[e + 1]), bf16x2(f[e + 2], f[e + 3]),
-                         bf16x2(f[e + 4], f[e + 5]), bf16x2(f[e + 6], f[e + 7]));
-      }
-      __syncwarp();
-      constexpr int kUnits = D / 8, kPer = 32 / kUnits;
-      const int c = lane % kUnits;
-#pragma unroll
-      for (int j = 0; j < kUnits; ++j) {
-        const int lr = tile_row + j * kPer + lane / kUnits;
-        if (lr < tile_rows) {
-          const int i = first + lr, b = i / G, h = g * G + (i - b * G);
-          *reinterpret_cast<uint4*>(a.out + (static_cast<int64_t>(r) * a.B + b) * a.out_stride +
-                                    h * D + c * 8) =
-              *reinterpret_cast<const uint4*>(qt + unit_at<D>(lr, c));
-        }
-      }
-    }
-  } else {
+  __syncwarp();
+  if (a.split > 1) {
     // ---------------------------------------------------------- joined output
-    // Partial rows [stream][row] of (o, m, l) in fp32 where the ring was.
-    float* part = reinterpret_cast<float*>(ring);
-    __syncthreads();  // every MMA and copy of this CTA has finished
-    if (active) {
-      float* o_row = part + (s * kRows + tile_row + lane) * P::kPitch;
-#pragma unroll
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
-        if (has_o) {
-          tmem_ld32(t_o + c, o);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0u;
-        }
-#pragma unroll
-        for (int e = 0; e < 32; e += 4)
-          *reinterpret_cast<uint4*>(o_row + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+    cluster_sync();
+    const Unit u = unit_of<kDual>(a, first_unit, rank);
+    const float* part = reinterpret_cast<const float*>(smem);
+    for (int i = rank * (kThreads / 32) + warp; i < u.rows; i += (kThreads / 32) * a.split) {
+      const float* mine = part + i * P::kPart;
+      float mp = kNegInf, lp = 0.f;
+      if (lane < a.split) {
+        const uint32_t at = peer_addr(mine, lane);
+        mp = ld_peer(at + D * 4);
+        lp = ld_peer(at + D * 4 + 4);
       }
-      o_row[D] = l > 0.f ? m : kNegInf;
-      o_row[D + 1] = l;
-    }
-    if (split > 1)
-      cluster_sync();
-    else
-      __syncthreads();
-    if (warp < 8) {
-      const int sources = dual ? split : 2 * split;
-      for (int i = rank * 8 + warp; i < rows; i += 8 * split) {
-        // Source p: rank p (two row tiles), or rank p / 2's stream p & 1.
-        auto at = [&](int p) {
-          const int st = dual ? i / kRows : p & 1;
-          return peer_addr(part + (st * kRows + i % kRows) * P::kPitch, dual ? p : p >> 1);
-        };
-        float mp = kNegInf, lp = 0.f;
-        if (lane < sources) {
-          mp = ld_peer(at(lane) + D * 4);
-          lp = ld_peer(at(lane) + D * 4 + 4);
+      const float top = warp_max(mp);
+      const float wt = mp > kNegInf ? ex2_approx(mp - top) : 0.f;
+      const float sum = warp_sum(wt * lp);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int p = 0; p < a.split; ++p) {
+        const float wp = __shfl_sync(0xFFFFFFFFu, wt, p);
+        if (wp > 0.f && lane < D / 4) {
+          const float4 v = ld_peer4(peer_addr(mine, p) + lane * 16);
+          o.x = fmaf(wp, v.x, o.x);
+          o.y = fmaf(wp, v.y, o.y);
+          o.z = fmaf(wp, v.z, o.z);
+          o.w = fmaf(wp, v.w, o.w);
         }
-        const float top = warp_max(mp);
-        const float w = mp > kNegInf ? ex2_approx(mp - top) : 0.f;
-        const float sum = warp_sum(w * lp);
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int p = 0; p < sources; ++p) {
-          const float wp = __shfl_sync(0xFFFFFFFFu, w, p);
-          if (wp > 0.f && lane < D / 4) {
-            const float4 v = ld_peer4(at(p) + lane * 16);
-            o.x = fmaf(wp, v.x, o.x);
-            o.y = fmaf(wp, v.y, o.y);
-            o.z = fmaf(wp, v.z, o.z);
-            o.w = fmaf(wp, v.w, o.w);
-          }
-        }
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
-        const int ii = row0 + i, b = ii / G, h = g * G + (ii - b * G);
-        if (lane < D / 4)
-          *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(r) * a.B + b) * a.out_stride +
-                                    h * D + lane * 4) =
-              make_uint2(bf16x2(o.x * inv, o.y * inv), bf16x2(o.z * inv, o.w * inv));
       }
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const int ii = u.row0 + i, b = ii / a.G, h = u.g * a.G + (ii - b * a.G);
+      if (lane < D / 4)
+        *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(u.r) * a.B + b) * a.out_stride +
+                                  h * D + lane * 4) =
+            make_uint2(bf16x2(o.x * inv, o.y * inv), bf16x2(o.z * inv, o.w * inv));
     }
-    if (split > 1) cluster_sync();  // no CTA leaves while its rows are read
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while its rows are read
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_free(tmem, 512);
+  if (warp == 13) tmem_free(tmem, 512);
 }
 
 // 4-D map of a cache [n_pages][page_size][Hkv][D], box [1][box][1][64].
-template <int D>
-bool make_map(CUtensorMap* map, const void* base, const AttnArgs& a, int box) {
+bool make_map(CUtensorMap* map, const void* base, const AttnArgs& a, int D, int box) {
   auto fn = tensor_map_encoder();
   if (!fn) return false;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(a.Hkv),
@@ -629,12 +956,12 @@ bool make_map(CUtensorMap* map, const void* base, const AttnArgs& a, int box) {
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
-int launch_attention(const AttnArgs& a, cudaStream_t stream) {
-  using P = Plan<D>;
+template <int D, bool kDual>
+int launch_attention(AttnArgs& a, cudaStream_t stream) {
+  using P = Plan<D, kDual>;
   CUtensorMap mk, mv;
   const int box = a.table ? std::min(a.page_size, kKeys) : kKeys;
-  if (!make_map<D>(&mk, a.k, a, box) || !make_map<D>(&mv, a.v, a, box))
+  if (!make_map(&mk, a.k, a, D, box) || !make_map(&mv, a.v, a, D, box))
     return set_error(SIDBEAM_ERR_CUDA, "beam_attention: tensor map encoding failed");
   static std::mutex mu;
   static bool done[64] = {};
@@ -644,34 +971,40 @@ int launch_attention(const AttnArgs& a, cudaStream_t stream) {
   {
     std::lock_guard<std::mutex> lock(mu);
     if (dev < 0 || dev >= 64 || !done[dev]) {
-      e = cudaFuncSetAttribute(attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               P::kSmem);
+      e = cudaFuncSetAttribute(attention_kernel<D, kDual>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
       if (e != cudaSuccess) return cuda_error(e, "beam_attention: cudaFuncSetAttribute");
       if (dev >= 0 && dev < 64) done[dev] = true;
     }
   }
-  const int all = a.B * (a.H / a.Hkv);
-  const int pairs = (all + 2 * kRows - 1) / (2 * kRows);
-  const int64_t items = static_cast<int64_t>(pairs) * a.Hkv * a.R;
+  const int sms = device_sm_count();
+  const int unit_rows = P::kTiles * kRows;
+  a.pairs = (a.B * a.G + unit_rows - 1) / unit_rows;
+  const int64_t units = static_cast<int64_t>(a.pairs) * a.Hkv * a.R;
+  if (units > 0x7FFFFFFFll - sms)
+    return set_error(SIDBEAM_ERR_INVALID_ARG, "beam_attention: too many rows and heads");
+  a.units = static_cast<int>(units);
   const int64_t cap = a.table ? static_cast<int64_t>(a.table_stride) * a.page_size : a.page_size;
   const int64_t max_tiles = (cap + kKeys - 1) / kKeys;
-  // CTAs per item: while they fit the SMs and each has two key tiles.
-  int split = 1;
-  while (split < kMaxSplit && items * split * 2 <= device_sm_count() && split * 4 <= max_tiles)
-    split *= 2;
+  // CTAs per unit: while they fit the SMs and each has two key tiles.
+  a.split_log2 = 0;
+  while (a.split_log2 < kMaxSplitLog2 && (units << (a.split_log2 + 1)) <= sms &&
+         (4 << a.split_log2) <= max_tiles)
+    ++a.split_log2;
+  a.split = 1 << a.split_log2;
   cudaLaunchConfig_t lc{};
-  lc.gridDim = dim3(static_cast<unsigned>(pairs * split * a.R), static_cast<unsigned>(a.Hkv));
+  lc.gridDim = dim3(static_cast<unsigned>(a.split > 1 ? a.units * a.split : std::min(a.units, sms)));
   lc.blockDim = dim3(kThreads);
   lc.dynamicSmemBytes = P::kSmem;
   lc.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = split;
+  attr[0].val.clusterDim.x = a.split;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   lc.attrs = attr;
-  lc.numAttrs = 1;
-  e = cudaLaunchKernelEx(&lc, attention_kernel<D>, mk, mv, a, pairs, split);
+  lc.numAttrs = a.split > 1 ? 1 : 0;
+  e = cudaLaunchKernelEx(&lc, attention_kernel<D, kDual>, mk, mv, a);
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? SIDBEAM_OK : cuda_error(e, "beam_attention: launch");
 }
@@ -762,10 +1095,22 @@ extern "C" int beam_attention(const void* q, int64_t q_row_stride, const void* k
   a.B = B;
   a.H = H;
   a.Hkv = Hkv;
-  a.scale_log2 = scale * kLog2e;
+  // A zero scale keeps a factor (it leaves every finite score 0 to within 2^-60):
+  // masked scores are -inf, and -inf * 0 is not.
+  a.scale_log2 = std::max(fabsf(scale) * kLog2e, 1e-30f);
+  a.q_flip = scale < 0.f ? 0x80008000u : 0u;
+  a.G = H / Hkv;
+  a.page_log2 = 0;
+  while (page_table && (1 << a.page_log2) < page_size) ++a.page_log2;
+  a.g_magic = a.G > 1 ? static_cast<uint32_t>((0x100000000ull + a.G - 1) / a.G) : 0u;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.out_stride = out_row_stride;
   a.status = static_cast<uint32_t*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return D == 64 ? launch_attention<64>(a, s) : launch_attention<128>(a, s);
+  // Two row tiles a unit where there are two; long paths need the table space
+  // that one tile leaves.
+  const bool dual = static_cast<int64_t>(B) * a.G > kRows && level <= 8;
+  if (D == 64)
+    return dual ? launch_attention<64, true>(a, s) : launch_attention<64, false>(a, s);
+  return dual ? launch_attention<128, true>(a, s) : launch_attention<128, false>(a, s);
 }

@@ -48,12 +48,6 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
   return bounded_wait(bar, parity, abort, status, kStatusTimeout);
 }
 
-// The whole warp waits; one answer for all lanes.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                          uint32_t* status) {
-  return __all_sync(0xFFFFFFFFu, wait(bar, parity, abort, status));
-}
-
 // ------------------------------------------------------------ many rows
 // Persistent over 128 x 256 tiles. Warp 0 loads (TMA), warp 1 issues MMAs, warps
 // 2-9 are the epilogue: the warp pair of a TMEM lane quarter takes 128 columns
@@ -133,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         drain_wait(&full[j % kStages], (j / kStages) & 1u);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       uint32_t it = 0;
       bool ok = true;
       for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
@@ -180,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ab = it & 1u;
         const uint64_t s2 = pack_f32x2(s, s);
         if (k + 1 < a.nb) s = sa[k + 1] * sw[k + 1];
-        if (!warp_wait(&acc_full[ab], (it >> 1) & 1u, abort_flag, a.status)) {
+        if (!warp_wait(&acc_full[ab], it >> 1, abort_flag, a.status)) {
           ok = false;
           break;
         }
@@ -330,7 +324,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         drain_wait(&full[j % stages], (j / stages) & 1u);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       for (int i = 0; i < n; ++i) {
         const int s = i % stages, ab = i % P::kAcc;
         if ((i >= P::kAcc &&
@@ -363,7 +357,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     const int quarter = warp & 3;
     for (int i = 0; i < n; ++i) {
       const int ab = i % P::kAcc;
-      if (!warp_wait(&acc_full[ab], (i / P::kAcc) & 1u, &abort_flag, a.status)) break;
+      if (!warp_wait(&acc_full[ab], i / P::kAcc, &abort_flag, a.status)) break;
       tc_fence_after();
       const uint32_t taddr = tmem + ab * NB + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll

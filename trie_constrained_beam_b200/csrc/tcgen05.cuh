@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "device_utils.cuh"
+#include "internal.h"
 
 namespace sidbeam {
 namespace dev {
@@ -22,6 +23,49 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
   return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1) << 16) |
          (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
          (static_cast<uint64_t>(2) << 61);
+}
+
+// Waits for a barrier's phase number `phase` (its parity), with the limits of
+// bounded_wait in fewer instructions: these kernels run several roles at once, and
+// their speed depends on all of their loops staying in the instruction cache. (Out
+// of line it costs more: with a call in the kernel the compiler keeps every role to
+// the registers of the launch, whatever setmaxnreg gives it.)
+// One thread:
+__device__ __forceinline__ bool lane_wait(uint64_t* bar, uint32_t phase, volatile int* abort,
+                                          uint32_t* status) {
+  uint64_t begun = 0;
+  while (!mbar_try_wait(bar, phase & 1u)) {
+    if (*abort) return false;
+    const uint64_t now = global_timer_ns();
+    if (begun == 0) begun = now;
+    if (now - begun > kWaitTimeoutNs) {
+      *abort = 1;
+      atomicOr(status, kStatusTimeout);
+      return false;
+    }
+  }
+  return true;
+}
+// The whole (converged) warp, one answer for all lanes. All lanes poll: one polling
+// lane that answers for the others measured 20-30% slower kernels.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t phase, volatile int* abort,
+                                          uint32_t* status) {
+  return __all_sync(0xFFFFFFFFu, lane_wait(bar, phase, abort, status));
+}
+
+// One lane of the (converged) warp, always the same one. Code that issues
+// tcgen05.mma stands behind this and not behind a lane number: the compiler then
+// knows that one lane runs it and keeps the descriptors in uniform registers.
+// Measured (128 x 128 x 16): 64 cycles per MMA, the tensor core's own rate,
+// against 134-166 behind `lane == 0`.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 
 // ------------------------------------------------------------ PTX wrappers
@@ -108,18 +152,14 @@ __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t* v) {
 __device__ __forceinline__ void tmem_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-// 32 consecutive 32-bit columns of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
+// 16 consecutive 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(
-          v[0]),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(v[0]),
       "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
       "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
-      "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]),
-      "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]),
-      "r"(v[30]), "r"(v[31]), "r"(taddr)
+      "r"(taddr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() {
@@ -191,6 +231,11 @@ __device__ __forceinline__ void unpack_f32x2(uint64_t v, float& lo, float& hi) {
 __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {

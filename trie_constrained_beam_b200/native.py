@@ -11,9 +11,12 @@ import ctypes
 import os
 
 import numpy as np
+import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libsidbeam.so")
+
+_BF16, _F32, _I32, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
 
 SIDBEAM_OK = 0
 SIDBEAM_ERR_INVALID_ARG = -1
@@ -136,7 +139,6 @@ def _stream(stream):
     """cudaStream_t of a torch stream; None means torch's current stream
     (or the legacy default stream when torch sees no device)."""
     if stream is None:
-        import torch
         if not torch.cuda.is_available():
             return None
         stream = torch.cuda.current_stream()
@@ -144,7 +146,6 @@ def _stream(stream):
 
 
 def _dtype_code(t):
-    import torch
     if t.dtype == torch.float32:
         return SIDBEAM_F32
     if t.dtype == torch.bfloat16:
@@ -343,34 +344,32 @@ def fused_lmhead_step(trie, step, hidden, w_sid, parent_scores, parent_nodes, R,
     _check(rc)
 
 
-def _need(t, name, dtype, shape=None, optional=False):
-    """Checks a tensor argument; returns its device address (None for an optional
-    argument left out). ``shape``: the exact shape of a contiguous tensor."""
+def _need(t, name, dtype, index, shape=None):
+    """Checks a tensor argument of device `index`; returns its address. ``shape``:
+    that of a contiguous tensor."""
     if t is None:
-        if optional:
-            return None
         raise ValueError(f"{name} is missing")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} dtype {t.dtype} is not {dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} is not on a CUDA device")
-    if shape is not None and (tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}, "
+    at = t.get_device()
+    if at != index or at < 0:
+        raise ValueError(f"{name} is on {t.device}, not on CUDA device {max(index, 0)}")
+    if shape is not None and (t.shape != shape or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous tensor of shape {shape}, "
                          f"got {tuple(t.shape)} with strides {t.stride()}")
     return t.data_ptr()
 
 
-def _same_device(first, *others):
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}")
+def _workspace(t, index):
+    """(address, bytes) of a workspace of any element type."""
+    if t.get_device() != index:
+        raise ValueError(f"workspace is on {t.device}, not on CUDA device {index}")
+    return t.data_ptr(), t.nbytes
 
 
-def _run_on(t, stream, fn, *args):
-    """Calls a C entry on the device of tensor `t`: on `stream`, or on that
-    device's current stream."""
-    import torch
-    index = t.device.index
+def _run_on(index, stream, fn, *args):
+    """Calls a C entry on CUDA device `index`: on `stream`, or on that device's
+    current stream."""
     s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
     if index == torch._C._cuda_getDevice():
         rc = fn(*args, s)
@@ -387,62 +386,47 @@ def residual_rmsnorm_fp8(x, residual, weight, eps, residual_out, hidden_q, hidde
     hidden_q e4m3 [M][d] with hidden_scale f32 [M][ceil(d/128)], a scale per 128
     columns. x, residual (or None) bf16 [M][d], weight bf16 [d]; residual_out
     (or None) receives h in bf16 and may be x or residual itself."""
-    import torch
-    M, d = x.shape
-    bf16 = torch.bfloat16
-    args = (_need(x, "x", bf16, (M, d)), _need(residual, "residual", bf16, (M, d), True),
-            _need(weight, "weight", bf16, (d,)), float(eps), M, d,
-            _need(residual_out, "residual_out", bf16, (M, d), True),
-            _need(hidden_q, "hidden_q", torch.float8_e4m3fn, (M, d)),
-            _need(hidden_scale, "hidden_scale", torch.float32, (M, -(-d // FP8_BLOCK))))
-    _same_device(x, residual, weight, residual_out, hidden_q, hidden_scale)
-    _run_on(x, stream, load().residual_rmsnorm_fp8, *args)
+    shape = M, d = x.shape
+    at = x.get_device()
+    _run_on(at, stream, load().residual_rmsnorm_fp8, _need(x, "x", _BF16, at, shape),
+            None if residual is None else _need(residual, "residual", _BF16, at, shape),
+            _need(weight, "weight", _BF16, at, (d,)), eps, M, d,
+            None if residual_out is None else _need(residual_out, "residual_out", _BF16, at, shape),
+            _need(hidden_q, "hidden_q", _E4M3, at, shape),
+            _need(hidden_scale, "hidden_scale", _F32, at, (M, -(-d // FP8_BLOCK))))
 
 
 def lmhead_quantize_fp8(w_sid, w_q, w_scale, stream=None):
     """The lm_head weight in 8 bits for lmhead_logits_fp8: w_sid bf16 [V][d] ->
     w_q e4m3 [V][d], w_scale f32 [ceil(V/128)][ceil(d/128)]."""
-    import torch
-    V, d = w_sid.shape
-    args = (_need(w_sid, "w_sid", torch.bfloat16, (V, d)), V, d,
-            _need(w_q, "w_q", torch.float8_e4m3fn, (V, d)),
-            _need(w_scale, "w_scale", torch.float32, (-(-V // FP8_BLOCK), -(-d // FP8_BLOCK))))
-    _same_device(w_sid, w_q, w_scale)
-    _run_on(w_sid, stream, load().lmhead_quantize_fp8, *args)
+    shape = V, d = w_sid.shape
+    at = w_sid.get_device()
+    _run_on(at, stream, load().lmhead_quantize_fp8, _need(w_sid, "w_sid", _BF16, at, shape), V, d,
+            _need(w_q, "w_q", _E4M3, at, shape),
+            _need(w_scale, "w_scale", _F32, at, (-(-V // FP8_BLOCK), -(-d // FP8_BLOCK))))
 
 
 def lmhead_logits_fp8(hidden_q, hidden_scale, w_q, w_scale, out, workspace, stream=None):
     """lmhead_logits on operands in 8 bits: out[row][c] = sum over blocks of 128
     columns of hidden_scale[row][b] * w_scale[c // 128][b] * <hidden_q, w_q>_b
     (fp32 accumulation). out f32 or bf16 [M][V], rows out.stride(0) apart."""
-    import torch
     M, d = hidden_q.shape
     V = w_q.shape[0]
     nb = -(-d // FP8_BLOCK)
-    e4m3, f32 = torch.float8_e4m3fn, torch.float32
-    if tuple(out.shape) != (M, V) or (V > 1 and out.stride(1) != 1):
+    at = hidden_q.get_device()
+    dtype = _dtype_code(out)
+    ld, col = out.stride()
+    if out.shape != (M, V) or (V > 1 and col != 1):
         raise ValueError(f"out must be [{M}, {V}] with unit column stride, got "
                          f"{tuple(out.shape)} with strides {out.stride()}")
-    # The stride of a single row means nothing: any aligned one serves.
-    ld = out.stride(0) if M > 1 else -(-V // 8) * 8
-    args = (_need(hidden_q, "hidden_q", e4m3, (M, d)),
-            _need(hidden_scale, "hidden_scale", f32, (M, nb)), _need(w_q, "w_q", e4m3, (V, d)),
-            _need(w_scale, "w_scale", f32, (-(-V // FP8_BLOCK), nb)), M, V, d,
-            _need(out, "out", out.dtype), _dtype_code(out), ld,
-            _need(workspace, "workspace", workspace.dtype),
-            workspace.numel() * workspace.element_size())
-    _same_device(hidden_q, hidden_scale, w_q, w_scale, out, workspace)
-    _run_on(hidden_q, stream, load().lmhead_logits_fp8, *args)
-
-
-def _heads(t, name, lead, D=None):
-    """A bf16 [..., heads, D] tensor whose last two axes are contiguous."""
-    import torch
-    if t.dim() != lead + 2 or (D is not None and t.shape[-1] != D):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}")
-    if t.stride(-1) != 1 or (t.shape[-2] > 1 and t.stride(-2) != t.shape[-1]):
-        raise ValueError(f"{name}: heads must be contiguous, got strides {t.stride()}")
-    return _need(t, name, torch.bfloat16)
+    if M <= 1:  # the stride of a single row means nothing: any aligned one serves
+        ld = -(-V // 8) * 8
+    _run_on(at, stream, load().lmhead_logits_fp8,
+            _need(hidden_q, "hidden_q", _E4M3, at, (M, d)),
+            _need(hidden_scale, "hidden_scale", _F32, at, (M, nb)),
+            _need(w_q, "w_q", _E4M3, at, (V, d)),
+            _need(w_scale, "w_scale", _F32, at, (-(-V // FP8_BLOCK), nb)), M, V, d,
+            _need(out, "out", out.dtype, at), dtype, ld, *_workspace(workspace, at))
 
 
 def beam_attention(q, k_cache, v_cache, cache_len, out, workspace, page_table=None, level=0,
@@ -458,46 +442,47 @@ def beam_attention(q, k_cache, v_cache, cache_len, out, workspace, page_table=No
                 int32 [depth, R, B] and of k_beam, v_beam bf16 [depth, R*B, Hkv, D]
     scale       default D ** -0.5
     """
-    import torch
-    i32 = torch.int32
     rows, H, D = q.shape
+    n_pages, page_size, Hkv, Dk = k_cache.shape
     R = cache_len.shape[0]
     B = rows // R if R else 0
-    Hkv = k_cache.shape[2]
+    at = q.get_device()
     if R < 1 or B * R != rows:
         raise ValueError(f"{rows} query rows for {R} requests")
     if v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride():
         raise ValueError("k_cache and v_cache differ in shape or strides")
-    if out.shape != q.shape:
-        raise ValueError("out and q differ in shape")
-    n_pages, page_size = k_cache.shape[0], k_cache.shape[1]
+    if out.shape != q.shape or Dk != D:
+        raise ValueError(f"shapes of q {tuple(q.shape)}, out {tuple(out.shape)} and k_cache "
+                         f"{tuple(k_cache.shape)} do not match")
+    q_row, q_head, q_one = q.stride()
+    o_row, o_head, o_one = out.stride()
+    page, token, k_head, k_one = k_cache.stride()
+    if (q_one != 1 or o_one != 1 or k_one != 1 or (H > 1 and (q_head != D or o_head != D))
+            or (Hkv > 1 and k_head != D)):
+        raise ValueError("the heads of a row must be contiguous in q, out and the caches")
+    # Axes of one element: their stride means nothing, the packed one serves.
+    if rows == 1:
+        q_row = o_row = H * D
+    if page_size == 1:
+        token = Hkv * D
+    if n_pages == 1:
+        page = page_size * token
     table, per, kb, vb, bp = None, 0, None, None, None
     if page_table is not None:
-        per = page_table.shape[1] if page_table.dim() == 2 else 0
-        table = _need(page_table, "page_table", i32, (R, per))
+        per = page_table.shape[-1]
+        table = _need(page_table, "page_table", _I32, at, (R, per))
     if level > 0:
-        depth = bp_parent.shape[0] if bp_parent is not None else 0
-        if depth < level:
-            raise ValueError(f"bp_parent holds {depth} steps, level is {level}")
-        bp = _need(bp_parent, "bp_parent", i32, (depth, R, B))
-        for t, name in ((k_beam, "k_beam"), (v_beam, "v_beam")):
+        for t, name in ((bp_parent, "bp_parent"), (k_beam, "k_beam"), (v_beam, "v_beam")):
             if t is None or t.shape[0] < level:
                 raise ValueError(f"{name} holds fewer than {level} levels")
-        kb = _need(k_beam, "k_beam", torch.bfloat16, (k_beam.shape[0], rows, Hkv, D))
-        vb = _need(v_beam, "v_beam", torch.bfloat16, (v_beam.shape[0], rows, Hkv, D))
-    # Axes of one element: their stride means nothing, the packed one serves.
-    token = k_cache.stride(1) if page_size > 1 else Hkv * D
-    page = k_cache.stride(0) if n_pages > 1 else max(page_size * token, Hkv * D)
-    args = (_heads(q, "q", 1), q.stride(0) if rows > 1 else H * D, _heads(k_cache, "k_cache", 2, D),
-            _heads(v_cache, "v_cache", 2, D), page, token, n_pages, page_size, table, per,
-            _need(cache_len, "cache_len", i32, (R,)), int(level), bp, kb, vb, R, B, H, Hkv, D,
-            D ** -0.5 if scale is None else float(scale), _heads(out, "out", 1, D),
-            out.stride(0) if rows > 1 else H * D, _need(workspace, "workspace", workspace.dtype),
-            workspace.numel() * workspace.element_size())
-    _same_device(q, k_cache, v_cache, cache_len, out, workspace, page_table)
-    if level > 0:
-        _same_device(q, k_beam, v_beam, bp_parent)
-    _run_on(q, stream, load().beam_attention, *args)
+        bp = _need(bp_parent, "bp_parent", _I32, at, (bp_parent.shape[0], R, B))
+        kb = _need(k_beam, "k_beam", _BF16, at, (k_beam.shape[0], rows, Hkv, D))
+        vb = _need(v_beam, "v_beam", _BF16, at, (v_beam.shape[0], rows, Hkv, D))
+    _run_on(at, stream, load().beam_attention, _need(q, "q", _BF16, at), q_row,
+            _need(k_cache, "k_cache", _BF16, at), _need(v_cache, "v_cache", _BF16, at), page, token,
+            n_pages, page_size, table, per, _need(cache_len, "cache_len", _I32, at, (R,)), level,
+            bp, kb, vb, R, B, H, Hkv, D, D ** -0.5 if scale is None else scale,
+            _need(out, "out", _BF16, at), o_row, *_workspace(workspace, at))
 
 
 def sidbeam_get_device_status(workspace, stream=None) -> int:
