@@ -168,6 +168,21 @@ def test_long_prompts_few_rows(tcb, R, B, S):
     assert torch.equal(first, c.out)   # joined in a fixed order
 
 
+@pytest.mark.parametrize("R,B,H,Hkv,D,level,page", [(250, 1, 4, 2, 128, 0, 16), (330, 2, 1, 1, 64, 1, 0),
+                                                    (80, 66, 4, 2, 64, 2, 0), (76, 67, 4, 2, 128, 1, 64)])
+def test_many_units(tcb, R, B, H, Hkv, D, level, page):
+    """More work items than SMs: every CTA runs several in a row, of all lengths
+    (none, one tile, odd and even tiles, ragged or not), in both row shapes."""
+    rng = np.random.default_rng(R)
+    lens = rng.choice([0, 1, 64, 100, 128, 129, 200, 256, 300, 384, 500], size=R)
+    c = Case(R, B, H, Hkv, D, lens, level=level, page=page, seed=R)
+    first = c.run(tcb).clone()
+    c.check()
+    c.run(tcb)
+    import torch
+    assert torch.equal(first, c.out)
+
+
 def test_group_of_128_heads(tcb):
     c = Case(2, 3, 128, 1, 64, [77, 300], level=1, seed=8)
     c.run(tcb)

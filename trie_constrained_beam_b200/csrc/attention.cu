@@ -70,7 +70,7 @@ constexpr float kNegInf = -INFINITY;
 // through distributed shared memory in rank order.
 constexpr int kRows = 128;
 constexpr int kKeys = 128;
-constexpr int kThreads = 512;  // softmax 0, softmax 1, rows, (TMA, MMA, -, -)
+constexpr int kThreads = 512;  // softmax 0, softmax 1, rows, (MMA, TMA, tails, -)
 constexpr int kMaxSplitLog2 = 3;
 constexpr uint16_t kNoSlot = 0xFFFFu;
 
@@ -82,8 +82,7 @@ struct Plan {
   static constexpr int kSlots = D == 128 ? (kDual ? 4 : 5) : 8;  // ring of K and V tiles
   static constexpr int kAhead = kDual ? 1 : 2;             // K tiles loaded before a V tile
   static constexpr int kLevels = kDual ? 8 : SIDBEAM_MAX_DEPTH;
-  static constexpr int kPitch = 36;                        // floats of a staged row (32 used)
-  static constexpr int kStage = 4 * 32 * kPitch * 4;       // 32 columns of each warp's rows
+  static constexpr int kStage = kRows * 128;               // 64 columns of a tile's rows, bf16
   static constexpr int kScores = kTiles * kRows * kLevels * 4;
   static constexpr int kSlotTab = kTiles * kRows * kLevels * 2;
   static constexpr int kMl = 2 * kRows * 8;
@@ -115,12 +114,12 @@ __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t addr, uint32_t half_by
 }
 
 struct Bars {
-  uint64_t full[8], empty[8];
-  uint64_t q_full[2], q_empty[2];    // Q tile of a stream in place / multiplied
+  uint64_t full[8], empty[8];        // ring slots: loaded / multiplied
+  uint64_t landed[8];                // a ragged V tile is in its slot, its tail not yet zero
+  uint64_t q_full[2], q_empty[2];    // a Q tile is in place / multiplied
   uint64_t s_full[2], p_ready[2];    // a step's scores / weights in TMEM
   uint64_t ml_full[2], o_full[2];    // a unit's row maxima and sums / O complete
   uint64_t o_empty[2];               // both have been read
-  uint64_t v_landed, v_clean;        // a ragged V tile is there / its tail is zero
   uint64_t drain;
   uint32_t tmem;
   int abort;
@@ -208,8 +207,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* ring = smem + P::kRing;
-  float* stage = reinterpret_cast<float*>(smem + P::kAfter);
-  float* scores = stage + P::kStage / 4;                        // [tiles][128][kLevels]
+  uint8_t* stage = smem + P::kAfter;
+  float* scores = reinterpret_cast<float*>(stage + P::kStage);  // [tiles][128][kLevels]
   uint16_t* slots = reinterpret_cast<uint16_t*>(scores + P::kScores / 4);
   float2* ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(slots) + P::kSlotTab);
   __shared__ Bars bar;
@@ -224,6 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < 8; ++s) {
       mbar_init(&bar.full[s], 1);
       mbar_init(&bar.empty[s], 1);
+      mbar_init(&bar.landed[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar.q_full[s], 4);
@@ -234,13 +234,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar.o_full[s], 1);
       mbar_init(&bar.o_empty[s], 4);
     }
-    mbar_init(&bar.v_landed, 1);
-    mbar_init(&bar.v_clean, 1);
     mbar_init(&bar.drain, 1);
     bar.abort = 0;
     fence_mbar_init();
   }
-  if (warp == 13) tmem_alloc(&bar.tmem, 512);
+  if (warp == 12) tmem_alloc(&bar.tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -252,6 +250,138 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 12) {
+      // -------------------------------------------------------- MMA issue
+      // One thread for both streams, in the order of the loads. (A thread per
+      // stream keeps the two in step, so that they want the exponentials, and then
+      // the tensor core, at the same time: measured 13% slower. And where it saw
+      // only its stream's slots it could take an older phase of a slot for the one
+      // it waits for: a wait tells phases apart by parity alone.)
+      if (elect_one()) {
+        bool ok = true;
+        auto wait = [&](uint64_t* b, int phase) {
+          ok = ok && lane_wait(b, static_cast<uint32_t>(phase), &bar.abort, a.status);
+        };
+        const uint32_t ring_at = smem_addr(ring);
+        const uint64_t q0 = smem_desc(smem_addr(smem));
+        // S of stream s from key tile t (counted over the CTA's units).
+        // `free`: the ring slot has no other user to come.
+        auto qk = [&](int s, int t, bool free) {
+          const int pos = pos_k(t, P::kAhead), slot = pos % P::kSlots;
+          wait(&bar.full[slot], pos / P::kSlots);
+          if (!ok) return;
+          tc_fence_after();
+          const uint64_t k = smem_desc(ring_at + slot * P::kTile);
+          const uint64_t q = q0 + (kDual && s ? P::kTile >> 4 : 0);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * P::kHalf + (kk & 3) * 32) >> 4;
+            umma_f16(tmem + s * kKeys, q + off, k + off, kIdescQK, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(&bar.s_full[s]);
+          if (free) umma_commit(&bar.empty[slot]);
+        };
+        // O of stream s += P V of key tile t, once step `count`'s weights are there.
+        auto pv = [&](int s, int t, int count, bool first, int done, bool free) {
+          const int pos = pos_v(t, P::kAhead), slot = pos % P::kSlots;
+          const uint64_t v = smem_desc_mn(ring_at + slot * P::kTile, P::kHalf);
+          wait(&bar.full[slot], pos / P::kSlots);
+          if (first && done > 0) wait(&bar.o_empty[s], done - 1);
+          wait(&bar.p_ready[s], count);
+          if (!ok) return;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            umma_f16_ts(tmem + 256 + s * 128, tmem + s * kKeys + kk * 8, v + kk * (2048 >> 4),
+                        idesc_pv(D), kk > 0 || !first ? 1u : 0u);
+          if (free) umma_commit(&bar.empty[slot]);
+        };
+        int base = 0, units = 0, units1 = 0;  // tiles and units behind (of stream 1)
+        int count0 = 0, count1 = 0;           // steps behind, of each stream
+        if constexpr (kDual) {
+          auto next = [&](int& w, Unit& u) {  // the next unit with key tiles
+            for (; w < a.units; w += stride) {
+              u = unit_of<kDual>(a, w, rank);
+              if (u.n > 0) {
+                w += stride;
+                return true;
+              }
+            }
+            return false;
+          };
+          int w = first_unit;
+          Unit u;
+          bool have = next(w, u);
+          bool begun0 = false, begun1 = false;  // the unit's first products are out
+          while (ok && have) {
+            const bool two = u.rows > kRows;
+            const int n = u.n;
+            if (!begun0) {
+              wait(&bar.q_full[0], units);
+              qk(0, base, !two);
+              if (n == 1) umma_commit(&bar.q_empty[0]);
+            }
+            if (two && !begun1) {
+              wait(&bar.q_full[1], units1);
+              qk(1, base, true);
+              if (n == 1) umma_commit(&bar.q_empty[1]);
+            }
+            begun0 = begun1 = false;
+            const bool more = next(w, u);
+            const bool two_next = more && u.rows > kRows;
+#pragma unroll 1
+            for (int e = 0; ok && e < 2 * n; ++e) {
+              // Step j of stream s, and the stream's next product behind it: of
+              // this unit, or the first of the next one.
+              const int j = e >> 1, s = e & 1;
+              if (s && !two) continue;
+              pv(s, base + j, s ? count1 : count0, j == 0, s ? units1 : units, s || !two);
+              if (s) ++count1; else ++count0;
+              if (!ok) break;
+              const bool last = j + 1 == n;
+              if (last) umma_commit(&bar.o_full[s]);
+              if (last && !(s ? two_next : more)) continue;
+              if (last) {
+                wait(&bar.q_full[s], (s ? units1 : units) + 1);
+                if (s) begun1 = true; else begun0 = true;
+              }
+              qk(s, base + j + 1, s || !(last ? two_next : two));
+              if (last ? u.n == 1 : j + 2 == n) umma_commit(&bar.q_empty[s]);
+            }
+            ++units;
+            if (two) ++units1;
+            base += n;
+            have = more;
+          }
+        } else {
+#pragma unroll 1
+          for (int w = first_unit; ok && w < a.units; w += stride) {
+            const Unit u = unit_of<kDual>(a, w, rank);
+            if (u.n == 0) continue;
+            wait(&bar.q_full[0], units);
+            // Two products ahead of the first weights, then in turn.
+#pragma unroll 1
+            for (int i = -2; ok && i < u.n; ++i) {
+              const int s = i & 1;
+              if (i >= 0) {
+                pv(s, base + i, s ? count1 : count0, i < 2, s ? units1 : units, true);
+                if (s) ++count1; else ++count0;
+                if (i + 2 >= u.n) umma_commit(&bar.o_full[s]);
+              }
+              if (ok && i + 2 < u.n) {
+                qk(s, base + i + 2, true);
+                if (i + 3 == u.n) umma_commit(&bar.q_empty[0]);
+              }
+            }
+            ++units;
+            if (u.n > 1) ++units1;
+            base += u.n;
+          }
+        }
+        umma_commit(&bar.drain);
+        drain_wait(&bar.drain, 0u);
+      }
+      __syncwarp();
+    } else if (warp == 13) {
       // -------------------------------------------------------- loads
       const int box = a.table ? min(a.page_size, kKeys) : kKeys;  // tokens of one copy
       const int boxes = kKeys / box;
@@ -310,11 +440,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         const int count = min(boxes, (c.u.len - tile * kKeys + box - 1) / box);
-        if (lane == 0) mbar_arrive_expect_tx(&bar.full[s], count * (D / 64) * box * 128);
+        // (A ragged V tile is handed on by the warp that clears its tail.)
+        uint64_t* to = !is_k && c.u.ragged && c.i == c.u.n - 1 ? &bar.landed[s] : &bar.full[s];
+        if (lane == 0) mbar_arrive_expect_tx(to, count * (D / 64) * box * 128);
         __syncwarp();
         if (issue)
           tma_load_4d(smem_addr(ring + s * P::kTile + my_half * P::kHalf + my_box * box * 128),
-                      is_k ? &map_k : &map_v, my_half * 64, c.u.g, at, page, &bar.full[s]);
+                      is_k ? &map_k : &map_v, my_half * 64, c.u.g, at, page, to);
         __syncwarp();
         top = pos + 1;
         if (is_k) {
@@ -336,138 +468,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           drain_wait(&bar.full[p % P::kSlots], (p / P::kSlots) & 1u);
       }
       __syncwarp();
-    } else if (warp == 13) {
-      // -------------------------------------------------------- MMA issue
-      if (elect_one()) {
-        bool ok = true;
-        auto wait = [&](uint64_t* b, int phase) {
-          ok = ok && lane_wait(b, static_cast<uint32_t>(phase), &bar.abort, a.status);
-        };
-        auto wait_load = [&](int pos) { wait(&bar.full[pos % P::kSlots], pos / P::kSlots); };
-        auto free_load = [&](int pos) { umma_commit(&bar.empty[pos % P::kSlots]); };
-        // One unit's place in the sequence: its key tiles follow `base` others.
-        struct Place {
-          Unit u;
-          int base, steps0, steps1, products;
-        };
-        int w = first_unit, tiles = 0;
-        auto next = [&](Place& p) {  // the next unit with key tiles
-          for (; w < a.units; w += stride) {
-            p.u = unit_of<kDual>(a, w, rank);
-            if (p.u.n > 0) {
-              w += stride;
-              p.base = tiles;
-              tiles += p.u.n;
-              p.steps0 = steps_of<kDual>(p.u, 0);
-              p.steps1 = steps_of<kDual>(p.u, 1);
-              p.products = 0;
-              return true;
-            }
-          }
-          p.steps0 = p.steps1 = 0;
-          return false;
-        };
-        int done0 = 0, done1 = 0;    // units behind, of each stream
-        int count0 = 0, count1 = 0;  // steps behind, of each stream
-        // S of step j of stream s: Q K^T.
-        auto product = [&](Place& p, int s, int j) {
-          const int pos = pos_k(p.base + tile_of<kDual>(s, j), P::kAhead);
-          if (j == 0) wait(&bar.q_full[kDual ? s : 0], kDual && s ? done1 : done0);
-          wait_load(pos);
-          if (!ok) return;
-          tc_fence_after();
-          const uint64_t q = smem_desc(smem_addr(smem + (kDual ? s : 0) * P::kTile));
-          const uint64_t k = smem_desc(smem_addr(ring + (pos % P::kSlots) * P::kTile));
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk >> 2) * P::kHalf + (kk & 3) * 32) >> 4;
-            umma_f16(tmem + s * kKeys, q + off, k + off, kIdescQK, kk > 0 ? 1u : 0u);
-          }
-          umma_commit(&bar.s_full[s]);
-          ++p.products;
-          if (kDual ? j + 1 == p.steps0 : p.products == p.u.n)
-            umma_commit(&bar.q_empty[kDual ? s : 0]);
-          if (!kDual || s == 1 || p.steps1 == 0) free_load(pos);
-        };
-        Place p, nx;
-        bool have = next(p);
-#pragma unroll 1
-        for (int s = 0; have && s < 2; ++s)
-          if ((s ? p.steps1 : p.steps0) > 0) product(p, s, 0);
-        int cleaned = 0;
-        while (ok && have) {
-          const bool more = next(nx);
-#pragma unroll 1
-          for (int e = 0; ok && e < 2 * p.steps0; ++e) {
-            const int j = e >> 1, s = e & 1;
-            const int steps = s ? p.steps1 : p.steps0;
-            if (j < steps) {
-              const int i = tile_of<kDual>(s, j);
-              const int pos = pos_v(p.base + i, P::kAhead);
-              const bool clean = p.u.ragged && i == p.u.n - 1 && (!kDual || s == 0);
-              if (clean) {
-                wait_load(pos);
-                mbar_arrive(&bar.v_landed);
-              }
-              wait(&bar.p_ready[s], s ? count1 : count0);
-              if (s) ++count1; else ++count0;
-              wait_load(pos);
-              if (clean) wait(&bar.v_clean, cleaned++);
-              const int done = s ? done1 : done0;
-              if (j == 0 && done > 0) wait(&bar.o_empty[s], done - 1);
-              if (!ok) break;
-              tc_fence_after();
-              const uint64_t v = smem_desc_mn(smem_addr(ring + (pos % P::kSlots) * P::kTile), P::kHalf);
-#pragma unroll
-              for (int kk = 0; kk < kKeys / 16; ++kk)
-                umma_f16_ts(tmem + 256 + s * 128, tmem + s * kKeys + kk * 8, v + kk * (2048 >> 4),
-                            idesc_pv(D), kk > 0 || j > 0 ? 1u : 0u);
-              if (!kDual || s == 1 || p.steps1 == 0) free_load(pos);
-            }
-            // The stream's next product: of this unit, or (at its last step, or
-            // at once where it has none) the first of the next unit.
-            Place* to = nullptr;
-            int to_j = 0;
-            if (j + 1 < steps) {
-              to = &p;
-              to_j = j + 1;
-            } else if (j + 1 == steps) {
-              umma_commit(&bar.o_full[s]);
-              if (s) ++done1; else ++done0;
-            }
-            if (kDual && !to && j + 1 == p.steps0 && (s ? nx.steps1 : nx.steps0) > 0) to = &nx;
-            if (to) product(*to, s, to_j);
-          }
-          if (!kDual)
-#pragma unroll 1
-            for (int s = 0; ok && s < 2; ++s)
-              if ((s ? nx.steps1 : nx.steps0) > 0) product(nx, s, 0);
-          p = nx;
-          have = more;
-        }
-        umma_commit(&bar.drain);
-        drain_wait(&bar.drain, 0u);
-      }
-      __syncwarp();
     } else if (warp == 14) {
       // -------------------------------------------------------- tails of V
       // Rows of V past a request's end may hold anything, and 0 * NaN is not 0:
-      // they are cleared between the copy and the product.
-      int tiles = 0, cleaned = 0;
+      // they are cleared between the copy and the products.
+      int tiles = 0;
+      uint32_t phases = 0u;  // of each slot's `landed`
       for (int w = first_unit; w < a.units; w += stride) {
         const Unit u = unit_of<kDual>(a, w, rank);
         tiles += u.n;
         if (!u.ragged) continue;
-        if (!warp_wait(&bar.v_landed, cleaned++, &bar.abort, a.status)) break;
-        uint8_t* vt = ring + (pos_v(tiles - 1, P::kAhead) % P::kSlots) * P::kTile;
+        const int vs = pos_v(tiles - 1, P::kAhead) % P::kSlots;
+        if (!warp_wait(&bar.landed[vs], phases >> vs & 1u, &bar.abort, a.status)) break;
+        phases ^= 1u << vs;
         constexpr int kUnits = D / 8;
 #pragma unroll 4
         for (int e = u.ragged * kUnits + lane; e < kKeys * kUnits; e += 32)
-          *reinterpret_cast<uint4*>(vt + unit_at(e / kUnits, e % kUnits)) =
+          *reinterpret_cast<uint4*>(ring + vs * P::kTile + unit_at(e / kUnits, e % kUnits)) =
               make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.v_clean);
+        if (lane == 0) mbar_arrive(&bar.full[vs]);
       }
     }
   } else if (warp < 8) {
@@ -568,211 +589,310 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------- rows
     // A warp keeps to the 32 rows of its TMEM lanes (of each tile) throughout, so
     // its pieces of Q, scores and staging need no barrier beyond the warp.
-    float* my_stage = stage + quarter * 32 * P::kPitch;
+    uint8_t* my_stage = stage + quarter * 32 * 128;
     const int my0 = quarter * 32;  // first of the warp's rows in a tile
     int done0 = 0, done1 = 0;      // units behind, of each stream
     bool ok = true;
-    auto beam_of = [&](int i) { return static_cast<int>(__umulhi(static_cast<uint32_t>(i), a.g_magic)); };
     // (2^32 / 1 does not fit the magic factor.)
-    auto split_row = [&](int i, int& b, int& h) {
-      b = a.G == 1 ? i : beam_of(i);
-      h = i - b * a.G;
+    auto beam_of = [&](int i) {
+      return a.G == 1 ? i : static_cast<int>(__umulhi(static_cast<uint32_t>(i), a.g_magic));
     };
-    auto rows_of = [&](const Unit& u, int tile) { return min(kRows, u.rows - tile * kRows); };
+    // The warp's valid rows of a tile.
+    auto rows_in = [&](const Unit& u, int tile) {
+      return min(32, u.rows - tile * kRows - my0);
+    };
+    // Elements from the row of the unit's first beam to this lane's row of a tile
+    // (strides are below 2^24, a unit has at most 256 beams).
+    auto row_off = [&](const Unit& u, int tile, int64_t row_stride) {
+      const int i = u.row0 + tile * kRows + my0 + lane, b = beam_of(i);
+      return static_cast<uint32_t>(b - beam_of(u.row0)) * static_cast<uint32_t>(row_stride) +
+             static_cast<uint32_t>((i - b * a.G) * D);
+    };
+    auto row_base = [&](const Unit& u, int64_t row_stride) {
+      return (static_cast<int64_t>(u.r) * a.B + beam_of(u.row0)) * row_stride + u.g * a.G * D;
+    };
+    // Row of [level][R * B][Hkv][D] for slot 0 of the unit's request and key head.
+    auto beam_base = [&](const Unit& u, int v) {
+      return ((static_cast<int64_t>(v) * a.R + u.r) * a.B * a.Hkv + u.g) * D;
+    };
 
     // Q of unit u into its tiles, behind the last product with the ones before.
     // (`more0`, `more1`: the unit before, not yet counted, used the stream.)
     auto load_q = [&](const Unit& u, int more0, int more1) {
-#pragma unroll 1
-      for (int t = 0; t < P::kTiles; ++t) {
-        const int users = t ? done1 + more1 : done0 + more0;
-        if (users > 0 && !warp_wait(&bar.q_empty[t], users - 1, &bar.abort, a.status)) ok = false;
-      }
-      if (!ok) return;
       constexpr int kUnits = D / 8, kPer = 32 / kUnits;
       const int c = lane % kUnits;
 #pragma unroll 1
       for (int t = 0; t < P::kTiles; ++t) {
+        const int users = t ? done1 + more1 : done0 + more0;
+        if (users > 0 && !warp_wait(&bar.q_empty[t], users - 1, &bar.abort, a.status)) ok = false;
+        if (!ok) return;
         uint8_t* qt = smem + t * P::kTile;
-        const int valid = rows_of(u, t);
-#pragma unroll 4
-        for (int j = 0; j < kUnits; ++j) {
-          const int lr = my0 + j * kPer + lane / kUnits;
-          if (lr < valid) {
-            int b, h;
-            split_row(u.row0 + t * kRows + lr, b, h);
-            cp_async16(qt + unit_at(lr, c), a.q + (static_cast<int64_t>(u.r) * a.B + b) * a.q_stride +
-                                                (u.g * a.G + h) * D + c * 8);
-          }
+        const int valid = rows_in(u, t);
+        const uint32_t off = row_off(u, t, a.q_stride);
+        const __nv_bfloat16* src = a.q + row_base(u, a.q_stride) + c * 8;
+#pragma unroll 1
+        for (int lr = lane / kUnits; lr < 32; lr += kPer) {
+          const uint32_t at = __shfl_sync(0xFFFFFFFFu, off, lr);
+          if (lr < valid) cp_async16(qt + unit_at(my0 + lr, c), src + at);
         }
-      }
-      cp_async_wait();
-      __syncwarp();
-      if (a.q_flip) {
-        for (int t = 0; t < P::kTiles; ++t)
+        cp_async_wait();
+        __syncwarp();
+        if (a.q_flip) {
 #pragma unroll 1
           for (int e = lane; e < 32 * kUnits; e += 32) {
-            uint4* q = reinterpret_cast<uint4*>(smem + t * P::kTile + unit_at(my0 + e / kUnits, e % kUnits));
+            uint4* q = reinterpret_cast<uint4*>(qt + unit_at(my0 + e / kUnits, e % kUnits));
             *q = make_uint4(q->x ^ a.q_flip, q->y ^ a.q_flip, q->z ^ a.q_flip, q->w ^ a.q_flip);
           }
-      }
-      fence_proxy_async();
-      __syncwarp();
-      for (int t = 0; t < P::kTiles; ++t)
+        }
+        fence_proxy_async();
+        __syncwarp();
         if (steps_of<kDual>(u, t) > 0 && lane == 0) mbar_arrive(&bar.q_full[t]);
+      }
     };
 
-    // Scores of the rows' ancestors, for the warp's rows of a tile: 16 rows by
-    // the (at most 16) beams they belong to, one level at a time, on the small
-    // tensor-core product; of the 16 x 8 block only a row's own beam is kept.
-    // The order of D inside the product is free as long as both sides share it,
-    // so each lane reads whole 16-byte words. Returns whether lane's row is dead.
-    auto score_path = [&](const Unit& u, int tile) {
-      const int valid = rows_of(u, tile) - my0;  // of this warp's rows
-      if (valid <= 0) return false;
-      uint16_t* tab = slots + (tile * kRows + my0) * P::kLevels;
-      float* xs = scores + (tile * kRows + my0) * P::kLevels;
-      const int i0 = u.row0 + tile * kRows + my0;
-      int b, h, at = -1;
-      if (lane < valid) {
-        split_row(i0 + lane, b, h);
-        at = b;
-      }
+    // The slots of the rows' ancestors at every level, both tiles' links followed
+    // together; a dead row has none. Returns a bit per tile: this lane's row is dead.
+    auto walk_path = [&](const Unit& u) {
+      int at[P::kTiles];
+#pragma unroll
+      for (int t = 0; t < P::kTiles; ++t)
+        at[t] = lane < rows_in(u, t) ? beam_of(u.row0 + t * kRows + my0 + lane) : -1;
 #pragma unroll 1
       for (int v = a.level - 1; v >= 0; --v) {
-        tab[lane * P::kLevels + v] = at < 0 ? kNoSlot : static_cast<uint16_t>(at);
-        if (at >= 0) {
-          const int p = a.bp[(static_cast<int64_t>(v) * a.R + u.r) * a.B + at];
-          at = p < 0 || (v > 0 && p >= a.B) ? -1 : p;
-        }
-      }
-      __syncwarp();
-      const int c = lane & 3, n8 = lane >> 2;
-      constexpr int kWords = D / 32;  // 16-byte words of a lane's quarter of D
-      const uint8_t* qt = smem + tile * P::kTile;
-#pragma unroll 1
-      for (int rg = 0; rg < 32 && rg < valid; rg += 16) {
-        uint4 qa[kWords], qb[kWords];
+        const int32_t* bp = a.bp + (static_cast<int64_t>(v) * a.R + u.r) * a.B;
+        int p[P::kTiles];
 #pragma unroll
-        for (int k = 0; k < kWords; ++k) {
-          qa[k] = *reinterpret_cast<const uint4*>(qt + unit_at(my0 + rg + n8, c * kWords + k));
-          qb[k] = *reinterpret_cast<const uint4*>(qt + unit_at(my0 + rg + n8 + 8, c * kWords + k));
+        for (int t = 0; t < P::kTiles; ++t) {
+          slots[(t * kRows + my0 + lane) * P::kLevels + v] = static_cast<uint16_t>(at[t]);
+          p[t] = at[t] < 0 ? -1 : bp[at[t]];
         }
-        int b0, b_lo, b_hi, b_end, hh;
-        split_row(i0 + rg, b0, hh);
-        split_row(i0 + rg + n8, b_lo, hh);
-        split_row(i0 + rg + n8 + 8, b_hi, hh);
-        split_row(i0 + min(rg + 15, valid - 1), b_end, hh);
+#pragma unroll
+        for (int t = 0; t < P::kTiles; ++t) at[t] = p[t] < 0 || (v > 0 && p[t] >= a.B) ? -1 : p[t];
+      }
+      uint32_t dead = 0u;
+#pragma unroll
+      for (int t = 0; t < P::kTiles; ++t)
+        if (at[t] < 0) {
+          dead |= 1u << t;
+          for (int v = 0; v < a.level; ++v)
+            slots[(t * kRows + my0 + lane) * P::kLevels + v] = kNoSlot;
+        }
+      __syncwarp();
+      return dead;
+    };
+
+    // The rows' own softmax over their ancestors, for the warp's rows of a tile,
+    // on the small tensor-core product: 16 rows by the (at most 16) beams that
+    // they belong to, of whose block only a row's own beam counts. The orders of D
+    // inside the products are free as long as both sides share them, so that each
+    // lane reads whole 16-byte words. (One row per lane instead measured 4 times
+    // the time: a lane's loads then touch 32 lines at once.) The weighted values,
+    // against the path's maximum, wait in the rows' places of the output (bf16);
+    // maximum and sum stay in the row's first two table entries.
+    auto attend_path = [&](const Unit& u, int tile, bool dead) {
+      const int valid = rows_in(u, tile);
+      if (valid <= 0) return;
+      const uint16_t* tab = slots + (tile * kRows + my0) * P::kLevels;
+      float* xs = scores + (tile * kRows + my0) * P::kLevels;
+      const int i0 = u.row0 + tile * kRows + my0;
+      const int c = lane & 3, n8 = lane >> 2;
+      const uint8_t* qt = smem + tile * P::kTile;
+      const int64_t key_stride = static_cast<int64_t>(a.Hkv) * D;
+      // ---- scores
+#pragma unroll 1
+      for (int rg = 0; rg < valid; rg += 16) {
+        constexpr int kWords = D / 32;  // 16-byte words of a lane's quarter of D
+        const int b0 = beam_of(i0 + rg), b_end = beam_of(i0 + min(rg + 15, valid - 1));
+        const int j_lo = beam_of(i0 + rg + n8) - b0, j_hi = beam_of(i0 + rg + n8 + 8) - b0;
 #pragma unroll 1
         for (int n0 = 0; n0 <= b_end - b0; n0 += 8) {
           // This lane's key: beam b0 + n0 + n8, through its first row in the group.
           const int kb = b0 + n0 + n8;
-          const int krow = max(rg, kb * a.G - i0);
+          const uint16_t* of = tab + max(rg, kb * a.G - i0) * P::kLevels;
 #pragma unroll 1
-          for (int v = 0; v < a.level; ++v) {
-            const uint16_t slot = kb <= b_end ? tab[krow * P::kLevels + v] : kNoSlot;
-            uint4 kw[kWords];
+          for (int v0 = 0; v0 < a.level; v0 += 4) {  // four levels' loads in flight
+            uint4 kw[4][kWords];
 #pragma unroll
-            for (int k = 0; k < kWords; ++k) kw[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (slot != kNoSlot) {
+            for (int e = 0; e < 4; ++e) {
+              const uint16_t slot = kb <= b_end && v0 + e < a.level ? of[v0 + e] : kNoSlot;
               const uint4* src = reinterpret_cast<const uint4*>(
-                  a.kb + (((static_cast<int64_t>(v) * a.R + u.r) * a.B + slot) * a.Hkv + u.g) * D +
-                  c * (D / 4));
+                  a.kb + beam_base(u, v0 + e) + slot * key_stride + c * (D / 4));
 #pragma unroll
-              for (int k = 0; k < kWords; ++k) kw[k] = src[k];
+              for (int k = 0; k < kWords; ++k) {
+                kw[e][k] = make_uint4(0u, 0u, 0u, 0u);
+                if (slot != kNoSlot) kw[e][k] = src[k];
+              }
             }
-            float z[4] = {0.f, 0.f, 0.f, 0.f};
+            float z[4][4] = {};
 #pragma unroll
             for (int k = 0; k < kWords; ++k) {
-              mma_16816(z, qa[k].x, qb[k].x, qa[k].y, qb[k].y, kw[k].x, kw[k].y);
-              mma_16816(z, qa[k].z, qb[k].z, qa[k].w, qb[k].w, kw[k].z, kw[k].w);
+              const uint4 qa =
+                  *reinterpret_cast<const uint4*>(qt + unit_at(my0 + rg + n8, c * kWords + k));
+              const uint4 qb =
+                  *reinterpret_cast<const uint4*>(qt + unit_at(my0 + rg + n8 + 8, c * kWords + k));
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                mma_16816(z[e], qa.x, qb.x, qa.y, qb.y, kw[e][k].x, kw[e][k].y);
+                mma_16816(z[e], qa.z, qb.z, qa.w, qb.w, kw[e][k].z, kw[e][k].w);
+              }
             }
-            const int j_lo = b_lo - b0 - n0, j_hi = b_hi - b0 - n0;
-            if (j_lo >= 0 && j_lo < 8 && (j_lo >> 1) == c)
-              xs[(rg + n8) * P::kLevels + v] = (j_lo & 1 ? z[1] : z[0]) * a.scale_log2;
-            if (j_hi >= 0 && j_hi < 8 && (j_hi >> 1) == c)
-              xs[(rg + n8 + 8) * P::kLevels + v] = (j_hi & 1 ? z[3] : z[2]) * a.scale_log2;
+            const int lo = j_lo - n0, hi = j_hi - n0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (v0 + e < a.level) {
+                if ((lo >> 1) == c)
+                  xs[(rg + n8) * P::kLevels + v0 + e] = (lo & 1 ? z[e][1] : z[e][0]) * a.scale_log2;
+                if ((hi >> 1) == c)
+                  xs[(rg + n8 + 8) * P::kLevels + v0 + e] =
+                      (hi & 1 ? z[e][3] : z[e][2]) * a.scale_log2;
+              }
+            }
           }
         }
       }
       __syncwarp();
-      return at < 0;
-    };
-
-    // 64 columns of the warp's rows: the path's share, then out.
-    auto write_half = [&](const Unit& u, const float (&o)[64], int h0, int valid, bool path,
-                          float* part, const uint16_t* tab, const float* ws, int i0) {
-      const int c4 = (lane & 7) * 4, r4 = lane >> 3;
-#pragma unroll
-      for (int c = 0; c < 64; c += 32) {
-        const int c0 = h0 + c;
-        // 32 columns through shared memory: from a row per lane to 8 lanes a row.
-#pragma unroll
-        for (int e = 0; e < 32; e += 4)
-          *reinterpret_cast<float4*>(my_stage + lane * P::kPitch + e) =
-              make_float4(o[c + e], o[c + e + 1], o[c + e + 2], o[c + e + 3]);
-        __syncwarp();
+      // ---- softmax, a row per lane
+      float mp = kNegInf, lp = 0.f;
+      {
+        float* x = xs + lane * P::kLevels;
+        if (!dead)
+          for (int v = 0; v < a.level; ++v) mp = fmaxf(mp, x[v]);
 #pragma unroll 1
-        for (int q = 0; q < 2; ++q) {
-          if (q * 16 >= valid) break;
-          float4 y[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            y[k] = *reinterpret_cast<const float4*>(my_stage + (q * 16 + k * 4 + r4) * P::kPitch + c4);
-          if (path) {
+        for (int v = 0; v < a.level; ++v) {
+          x[v] = dead ? 0.f : ex2_approx(x[v] - mp);
+          lp += x[v];
+        }
+      }
+      __syncwarp();
+      // ---- values
+      const uint32_t off = row_off(u, tile, a.out_stride);
+      __nv_bfloat16* out = a.out + row_base(u, a.out_stride);
 #pragma unroll 1
-            for (int v = 0; v < a.level; ++v) {
-              const __nv_bfloat16* src =
-                  a.vb + ((static_cast<int64_t>(v) * a.R + u.r) * a.B * a.Hkv + u.g) * D + c0 + c4;
-              uint2 vw[4];
+      for (int rg = 0; rg < valid; rg += 16) {
+        constexpr int kCols = D / 8;         // columns a lane reads of a key; n blocks
+        constexpr int kWords = kCols / 2;    // their 32-bit words
+        float y[kCols][4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint16_t slot = tab[(q * 16 + k * 4 + r4) * P::kLevels + v];
-                vw[k] = make_uint2(0u, 0u);
-                if (slot != kNoSlot)
-                  vw[k] = *reinterpret_cast<const uint2*>(src + static_cast<int64_t>(slot) * a.Hkv * D);
-              }
+        for (int k = 0; k < kCols; ++k)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float wt = ws[(q * 16 + k * 4 + r4) * P::kLevels + v];
-                float vf[4];
-                bf16x4(vw[k], vf);
-                if (wt > 0.f) {
-                  y[k].x = fmaf(wt, vf[0], y[k].x);
-                  y[k].y = fmaf(wt, vf[1], y[k].y);
-                  y[k].z = fmaf(wt, vf[2], y[k].z);
-                  y[k].w = fmaf(wt, vf[3], y[k].w);
-                }
+          for (int e = 0; e < 4; ++e) y[k][e] = 0.f;
+        const int b0 = beam_of(i0 + rg), b_end = beam_of(i0 + min(rg + 15, valid - 1));
+        const int j_lo = beam_of(i0 + rg + n8) - b0, j_hi = beam_of(i0 + rg + n8 + 8) - b0;
+#pragma unroll 1
+        for (int n0 = 0; n0 <= b_end - b0; n0 += 8) {
+#pragma unroll 1
+          for (int v0 = 0; v0 < a.level; v0 += 2) {
+            // Keys of this lane: beams b0 + n0 + 2c, + 1 at levels v0, v0 + 1.
+            uint32_t vw[4][kWords];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int kb = b0 + n0 + 2 * c + (e & 1), v = v0 + (e >> 1);
+              const uint16_t slot = kb <= b_end && v < a.level
+                                        ? tab[max(rg, kb * a.G - i0) * P::kLevels + v]
+                                        : kNoSlot;
+              const uint4* src = reinterpret_cast<const uint4*>(
+                  a.vb + beam_base(u, v) + slot * key_stride + n8 * kCols);
+#pragma unroll
+              for (int k = 0; k < kWords; k += 4) {
+                uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                if (slot != kNoSlot) w = src[k / 4];
+                vw[e][k] = w.x;
+                vw[e][k + 1] = w.y;
+                vw[e][k + 2] = w.z;
+                vw[e][k + 3] = w.w;
               }
             }
-          }
+            // Weights: a row's in the place of its own beam, as the sum of two bf16
+            // (its values are rounded once on their way through the output, and
+            // that takes what rounding the weights are allowed).
+            const int lo = j_lo - n0, hi = j_hi - n0;
+            uint32_t aw[4], ar[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int lr = q * 16 + k * 4 + r4;
-            if (lr < valid) {
-              if (a.split > 1) {
-                *reinterpret_cast<float4*>(part + lr * P::kPart + c0 + c4) = y[k];
-              } else {
-                int b, h;
-                split_row(i0 + lr, b, h);
-                *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(u.r) * a.B + b) * a.out_stride +
-                                          (u.g * a.G + h) * D + c0 + c4) =
-                    make_uint2(bf16x2(y[k].x, y[k].y), bf16x2(y[k].z, y[k].w));
-              }
+            for (int e = 0; e < 4; ++e) {
+              const int at = e & 1 ? hi : lo, v = v0 + (e >> 1);
+              const float wt = (at >> 1) == c && v < a.level
+                                   ? xs[(rg + n8 + (e & 1) * 8) * P::kLevels + v]
+                                   : 0.f;
+              const float head = __uint_as_float(__float_as_uint(wt) & 0xFFFF0000u);
+              aw[e] = at & 1 ? bf16x2(0.f, head) : bf16x2(head, 0.f);
+              ar[e] = at & 1 ? bf16x2(0.f, wt - head) : bf16x2(wt - head, 0.f);
+            }
+#pragma unroll
+            for (int k = 0; k < kWords; ++k) {
+              const uint32_t e0 = __byte_perm(vw[0][k], vw[1][k], 0x5410);
+              const uint32_t e1 = __byte_perm(vw[2][k], vw[3][k], 0x5410);
+              const uint32_t o0 = __byte_perm(vw[0][k], vw[1][k], 0x7632);
+              const uint32_t o1 = __byte_perm(vw[2][k], vw[3][k], 0x7632);
+              mma_16816(y[2 * k], aw[0], aw[1], aw[2], aw[3], e0, e1);
+              mma_16816(y[2 * k], ar[0], ar[1], ar[2], ar[3], e0, e1);
+              mma_16816(y[2 * k + 1], aw[0], aw[1], aw[2], aw[3], o0, o1);
+              mma_16816(y[2 * k + 1], ar[0], ar[1], ar[2], ar[3], o0, o1);
             }
           }
         }
-        __syncwarp();
+        // An infinity or NaN in one beam's values would reach its neighbours
+        // through their zero weights: such a group is added up row by row.
+        float all = 0.f;
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) all += (y[k][0] + y[k][1]) + (y[k][2] + y[k][3]);
+        if (__any_sync(0xFFFFFFFFu, !(fabsf(all) < 3.0e38f))) {
+#pragma unroll 1
+          for (int lr = rg; lr < min(rg + 16, valid); ++lr) {
+            const uint32_t at = __shfl_sync(0xFFFFFFFFu, off, lr);
+#pragma unroll 1
+            for (int d = lane; d < D; d += 32) {
+              float z = 0.f;
+              for (int v = 0; v < a.level; ++v) {
+                const uint16_t slot = tab[lr * P::kLevels + v];
+                if (slot != kNoSlot)
+                  z = fmaf(xs[lr * P::kLevels + v],
+                           __bfloat162float(a.vb[beam_base(u, v) + slot * key_stride + d]), z);
+              }
+              out[at + d] = __float2bfloat16(z);
+            }
+          }
+        } else {
+          // This lane: D / 4 consecutive columns of rows rg + n8 and + 8.
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int lr = rg + n8 + half * 8;
+            const uint32_t at = __shfl_sync(0xFFFFFFFFu, off, lr);
+            if (lr < valid) {
+              uint4* dst = reinterpret_cast<uint4*>(out + at + c * (D / 4));
+#pragma unroll
+              for (int q = 0; q < 2; ++q)  // columns of n = 2c, then of n = 2c + 1
+#pragma unroll
+                for (int k = 0; k < kCols; k += 8) {
+                  const int e = half * 2 + q;
+                  dst[(q * kCols + k) / 8] =
+                      make_uint4(bf16x2(y[k][e], y[k + 1][e]), bf16x2(y[k + 2][e], y[k + 3][e]),
+                                 bf16x2(y[k + 4][e], y[k + 5][e]), bf16x2(y[k + 6][e], y[k + 7][e]));
+                }
+            }
+          }
+        }
       }
+      __syncwarp();
+      xs[lane * P::kLevels] = mp;
+      xs[lane * P::kLevels + 1] = lp;
     };
 
-    // Joins the streams and the path of the warp's rows of a tile, and writes
-    // them: bf16 rows, or (split keys) partial rows in fp32.
+    // Joins the streams and the path of the warp's rows of a tile, a row per lane,
+    // and writes them: bf16 rows, or (split keys) partial rows in fp32.
     auto finish = [&](const Unit& u, int tile, bool dead) {
-      const int valid = rows_of(u, tile) - my0;
+      const int valid = rows_in(u, tile);
       const int s_end = kDual ? tile + 1 : 2;
       const bool path = a.level > 0 && rank == 0;
-      float* xs = scores + (tile * kRows + my0 + lane) * P::kLevels;
+      const uint32_t off = row_off(u, tile, a.out_stride);
+      __nv_bfloat16* out = a.out + row_base(u, a.out_stride);
+      float mp = kNegInf, lp = 0.f;
+      if (path && lane < valid) {
+        const float* x = scores + (tile * kRows + my0 + lane) * P::kLevels;
+        mp = x[0];
+        lp = x[1];
+        for (int c = 0; c < D; c += 64)
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(out + off + c));
+      }
       float2 st_a = make_float2(kNegInf, 0.f), st_b = st_a;
 #pragma unroll 1
       for (int s = kDual ? tile : 0; s < s_end; ++s) {
@@ -787,78 +907,98 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (kDual || s == 0) st_a = got; else st_b = got;
       }
       tc_fence_after();
-      float top = kNegInf, sum = 0.f, f0 = 0.f, f1 = 0.f;
-      if (valid > 0) {
-        // Weights: one reference for all sources of the row.
-        top = fmaxf(st_a.y > 0.f ? st_a.x : kNegInf, st_b.y > 0.f ? st_b.x : kNegInf);
-        if (path)
-#pragma unroll 1
-          for (int v = 0; v < a.level; ++v) top = fmaxf(top, xs[v]);
-        const float ref = top > kNegInf ? top : 0.f;
-        f0 = st_a.y > 0.f ? ex2_approx(st_a.x - ref) : 0.f;
-        f1 = st_b.y > 0.f ? ex2_approx(st_b.x - ref) : 0.f;
-        sum = f0 * st_a.y + f1 * st_b.y;
-        if (path)
-#pragma unroll 1
-          for (int v = 0; v < a.level; ++v) {
-            xs[v] = ex2_approx(xs[v] - ref);
-            sum += xs[v];
-          }
-        if (dead) {
-          sum = 0.f;
-          top = kNegInf;
-        }
-        const float inv = a.split > 1 ? (dead ? 0.f : 1.f) : (sum > 0.f ? 1.f / sum : 0.f);
+      // One reference for all sources of the row. (l > 0 is false for NaN, which
+      // the q of a dead row may lead to.)
+      const bool has_a = st_a.y > 0.f && !dead, has_b = st_b.y > 0.f && !dead;
+      const bool has_p = lp > 0.f && !dead;
+      const float top = fmaxf(fmaxf(has_a ? st_a.x : kNegInf, has_b ? st_b.x : kNegInf),
+                              has_p ? mp : kNegInf);
+      const float ref = top > kNegInf ? top : 0.f;
+      float f0 = has_a ? ex2_approx(st_a.x - ref) : 0.f;
+      float f1 = has_b ? ex2_approx(st_b.x - ref) : 0.f;
+      float fp = has_p ? ex2_approx(mp - ref) : 0.f;
+      const float sum = f0 * st_a.y + f1 * st_b.y + fp * lp;
+      const float total = has_a || has_b || has_p ? sum : 0.f;
+      if (a.split == 1) {
+        const float inv = total > 0.f ? 1.f / total : 0.f;
         f0 *= inv;
         f1 *= inv;
-        if (path)
-#pragma unroll 1
-          for (int v = 0; v < a.level; ++v) xs[v] = dead ? 0.f : xs[v] * inv;
+        fp *= inv;
       }
-      float* part = reinterpret_cast<float*>(smem) + (tile * kRows + my0) * P::kPart;
+      float* part = reinterpret_cast<float*>(smem) + (tile * kRows + my0 + lane) * P::kPart;
       if (a.split > 1 && valid > 0) {
-        part[lane * P::kPart + D] = top;
-        part[lane * P::kPart + D + 1] = sum;
+        part[D] = top;
+        part[D + 1] = total;
       }
+      uint32_t packed[D / 2];
       const int sa = kDual ? tile : 0;
-      const bool has_a = steps_of<kDual>(u, sa) > 0, has_b = !kDual && steps_of<kDual>(u, 1) > 0;
-      const uint16_t* tab = slots + (tile * kRows + my0) * P::kLevels;
-      const float* ws = scores + (tile * kRows + my0) * P::kLevels;
-      const int i0 = u.row0 + tile * kRows + my0;
-#pragma unroll 1
-      for (int h0 = 0; h0 < D; h0 += 64) {
-        float o[64];
 #pragma unroll
-        for (int e = 0; e < 64; ++e) o[e] = 0.f;
-        if (valid > 0 && has_a) {
-          const uint32_t t_o = tmem + 256 + sa * 128 + quad + h0;
-          tmem_ld32_async(t_o, reinterpret_cast<uint32_t*>(o));
-          tmem_ld32_async(t_o + 32, reinterpret_cast<uint32_t*>(o) + 32);
-          tmem_wait_ld();
-          // A dead row's q may hold anything, its O then too.
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
 #pragma unroll
-          for (int e = 0; e < 64; ++e) o[e] = dead ? 0.f : o[e] * f0;
+        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+        if (valid > 0 && steps_of<kDual>(u, sa) > 0) {
+          uint32_t v[32];
+          tmem_ld32(tmem + 256 + sa * 128 + quad + c, v);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = has_a ? __uint_as_float(v[e]) * f0 : 0.f;
         }
-        if (valid > 0 && has_b) {
+        if (!kDual && valid > 0 && steps_of<kDual>(u, 1) > 0) {
+          uint32_t v[32];
+          tmem_ld32(tmem + 256 + 128 + quad + c, v);
 #pragma unroll
-          for (int c = 0; c < 64; c += 16) {
-            uint32_t v[16];
-            tmem_ld16(tmem + 256 + 128 + quad + h0 + c, v);
+          for (int e = 0; e < 32; ++e)
+            if (has_b) o[e] = fmaf(__uint_as_float(v[e]), f1, o[e]);
+        }
+        if (fp > 0.f && lane < valid) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              o[c + e] = dead ? 0.f : fmaf(__uint_as_float(v[e]), f1, o[c + e]);
+          for (int e = 0; e < 32; e += 8) {
+            const uint4 w = *reinterpret_cast<const uint4*>(out + off + c + e);
+            float f[4];
+            bf16x4(make_uint2(w.x, w.y), f);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[e + k] = fmaf(fp, f[k], o[e + k]);
+            bf16x4(make_uint2(w.z, w.w), f);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[e + 4 + k] = fmaf(fp, f[k], o[e + 4 + k]);
           }
         }
-        if (h0 + 64 == D) {  // O has been read
-          tc_fence_before();
-          __syncwarp();
-          for (int s = kDual ? tile : 0; s < s_end; ++s)
-            if (steps_of<kDual>(u, s) > 0) {
-              if (lane == 0) mbar_arrive(&bar.o_empty[s]);
-              if (s) ++done1; else ++done0;
-            }
+        if (a.split > 1 && valid > 0) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(part + c + e) =
+                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
-        if (valid > 0) write_half(u, o, h0, valid, path, part, tab, ws, i0);
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) packed[(c + e) / 2] = bf16x2(o[e], o[e + 1]);
+      }
+      // O has been read.
+      tc_fence_before();
+      __syncwarp();
+      for (int s = kDual ? tile : 0; s < s_end; ++s)
+        if (steps_of<kDual>(u, s) > 0) {
+          if (lane == 0) mbar_arrive(&bar.o_empty[s]);
+          if (s) ++done1; else ++done0;
+        }
+      if (a.split > 1 || valid <= 0) return;
+      // From a row per lane to whole 128-byte lines of the output.
+      const int u8 = lane & 7;
+#pragma unroll
+      for (int c = 0; c < D; c += 64) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<uint4*>(my_stage + lane * 128 + (((k ^ lane) & 7) << 4)) =
+              make_uint4(packed[c / 2 + k * 4], packed[c / 2 + k * 4 + 1],
+                         packed[c / 2 + k * 4 + 2], packed[c / 2 + k * 4 + 3]);
+        __syncwarp();
+#pragma unroll 4
+        for (int lr = lane >> 3; lr < 32; lr += 4) {
+          const uint32_t at = __shfl_sync(0xFFFFFFFFu, off, lr);
+          const uint4 w =
+              *reinterpret_cast<const uint4*>(my_stage + lr * 128 + (((u8 ^ lr) & 7) << 4));
+          if (lr < valid) *reinterpret_cast<uint4*>(out + at + c + u8 * 8) = w;
+        }
+        __syncwarp();
       }
     };
 
@@ -869,26 +1009,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int w = first_unit; ok && w < a.units; w += stride) {
       uint32_t dead = 0u;  // bit t: this lane's row of tile t
-      if (a.level > 0)
+      if (a.level > 0) {
+        dead = walk_path(u);
 #pragma unroll 1
-        for (int t = 0; t * kRows < u.rows; ++t)
-          if (score_path(u, t)) dead |= 1u << t;
-      // done[] still counts the units before this one: its Q is in use until its
-      // own products are done, which is what the next load waits for.
+        for (int t = 0; rank == 0 && t * kRows < u.rows; ++t)
+          attend_path(u, t, (dead >> t & 1u) != 0u);
+      }
+      // The next unit's Q comes in once this one's last products are done.
       const int w2 = w + stride;
       Unit nx = u;
       if (w2 < a.units) {
         nx = unit_of<kDual>(a, w2, rank);
         load_q(nx, steps_of<kDual>(u, 0) > 0, steps_of<kDual>(u, 1) > 0);
       }
-      if (ok && a.split > 1 && kDual) {
-        // Partial rows go where Q and the ring are: both streams end first.
+      if (a.split > 1) {
+        // Partial rows go where Q and the ring are: both streams end first, and
+        // every warp has read Q. (One unit only: all four warps come here.)
         for (int s = 0; s < 2; ++s)
           if (steps_of<kDual>(u, s) > 0 &&
               !warp_wait(&bar.o_full[s], s ? done1 : done0, &bar.abort, a.status))
             ok = false;
+        named_sync(1, 128);
       }
-      if (a.split > 1) named_sync(1, 128);  // one unit only; every warp has read Q
 #pragma unroll 1
       for (int t = 0; ok && t * kRows < u.rows; ++t) finish(u, t, (dead >> t & 1u) != 0u);
       u = nx;
@@ -936,7 +1078,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 13) tmem_free(tmem, 512);
+  if (warp == 12) tmem_free(tmem, 512);
 }
 
 // 4-D map of a cache [n_pages][page_size][Hkv][D], box [1][box][1][64].
@@ -1065,6 +1207,8 @@ extern "C" int beam_attention(const void* q, int64_t q_row_stride, const void* k
   if (q_row_stride < row || out_row_stride < row ||
       token_stride < static_cast<int64_t>(Hkv) * D || page_stride < token_stride)
     return set_error(SIDBEAM_ERR_INVALID_ARG, "beam_attention: a stride is smaller than its row");
+  if (q_row_stride >= 1 << 24 || out_row_stride >= 1 << 24)
+    return set_error(SIDBEAM_ERR_INVALID_ARG, "beam_attention: a row stride is 2^24 or more");
   if (page_stride > (1ll << 38))
     return set_error(SIDBEAM_ERR_INVALID_ARG, "beam_attention: page_stride too large");
   if (misaligned(q, 16) || misaligned(k_cache, 16) || misaligned(v_cache, 16) ||
