@@ -48,6 +48,7 @@ struct AttnArgs {
   int pairs, units;
   int split, split_log2;
   int page_log2;      // of page_size (with a page table)
+  uint32_t level16;   // 16-byte words of a level of k_beam, v_beam
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -72,7 +73,6 @@ constexpr int kRows = 128;
 constexpr int kKeys = 128;
 constexpr int kThreads = 512;  // softmax 0, softmax 1, rows, (MMA, TMA, tails, -)
 constexpr int kMaxSplitLog2 = 3;
-constexpr uint16_t kNoSlot = 0xFFFFu;
 
 template <int D, bool kDual>
 struct Plan {
@@ -82,7 +82,7 @@ struct Plan {
   static constexpr int kSlots = D == 128 ? (kDual ? 4 : 5) : 8;  // ring of K and V tiles
   static constexpr int kAhead = kDual ? 1 : 2;             // K tiles loaded before a V tile
   static constexpr int kLevels = kDual ? 8 : SIDBEAM_MAX_DEPTH;
-  static constexpr int kStage = kRows * 128;               // 64 columns of a tile's rows, bf16
+  static constexpr int kStage = kRows * 64;                // 32 columns of a tile's rows, bf16
   static constexpr int kScores = kTiles * kRows * kLevels * 4;
   static constexpr int kSlotTab = kTiles * kRows * kLevels * 2;
   static constexpr int kMl = 2 * kRows * 8;
@@ -242,11 +242,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = bar.tmem;
+  // All 512 columns are this CTA's, so they begin at column 0.
+  constexpr uint32_t tmem = 0u;
   const int quarter = warp & 3;
   const uint32_t quad = static_cast<uint32_t>(quarter * 32) << 16;  // a warp's TMEM lanes
 
-  // Registers: 512 threads start with 128 each; 168 + 168 + 120 + 56 = 4 * 128.
+  // Registers: 512 threads start with 128 each; 160 + 160 + 136 + 56 = 4 * 128.
   if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 12) {
@@ -256,10 +257,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the tensor core, at the same time: measured 13% slower. And where it saw
       // only its stream's slots it could take an older phase of a slot for the one
       // it waits for: a wait tells phases apart by parity alone.)
-      if (elect_one()) {
+      // The warp goes together and one lane issues: what is the same for all
+      // lanes can then live in uniform registers, where the instruction wants it.
+      {
         bool ok = true;
         auto wait = [&](uint64_t* b, int phase) {
-          ok = ok && lane_wait(b, static_cast<uint32_t>(phase), &bar.abort, a.status);
+          ok = ok && warp_wait(b, static_cast<uint32_t>(phase), &bar.abort, a.status);
+        };
+        auto commit = [&](uint64_t* b) {
+          if (elect_one()) umma_commit(b);
+          __syncwarp();
         };
         const uint32_t ring_at = smem_addr(ring);
         const uint64_t q0 = smem_desc(smem_addr(smem));
@@ -272,13 +279,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint64_t k = smem_desc(ring_at + slot * P::kTile);
           const uint64_t q = q0 + (kDual && s ? P::kTile >> 4 : 0);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk >> 2) * P::kHalf + (kk & 3) * 32) >> 4;
-            umma_f16(tmem + s * kKeys, q + off, k + off, kIdescQK, kk > 0 ? 1u : 0u);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = ((kk >> 2) * P::kHalf + (kk & 3) * 32) >> 4;
+              umma_f16(tmem + s * kKeys, q + off, k + off, kIdescQK, kk > 0 ? 1u : 0u);
+            }
+            umma_commit(&bar.s_full[s]);
+            if (free) umma_commit(&bar.empty[slot]);
           }
-          umma_commit(&bar.s_full[s]);
-          if (free) umma_commit(&bar.empty[slot]);
+          __syncwarp();
         };
         // O of stream s += P V of key tile t, once step `count`'s weights are there.
         auto pv = [&](int s, int t, int count, bool first, int done, bool free) {
@@ -289,11 +299,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait(&bar.p_ready[s], count);
           if (!ok) return;
           tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk)
-            umma_f16_ts(tmem + 256 + s * 128, tmem + s * kKeys + kk * 8, v + kk * (2048 >> 4),
-                        idesc_pv(D), kk > 0 || !first ? 1u : 0u);
-          if (free) umma_commit(&bar.empty[slot]);
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              umma_f16_ts(tmem + 256 + s * 128, tmem + s * kKeys + kk * 8, v + kk * (2048 >> 4),
+                          idesc_pv(D), kk > 0 || !first ? 1u : 0u);
+            if (free) umma_commit(&bar.empty[slot]);
+          }
+          __syncwarp();
         };
         int base = 0, units = 0, units1 = 0;  // tiles and units behind (of stream 1)
         int count0 = 0, count1 = 0;           // steps behind, of each stream
@@ -315,38 +328,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           while (ok && have) {
             const bool two = u.rows > kRows;
             const int n = u.n;
-            if (!begun0) {
-              wait(&bar.q_full[0], units);
-              qk(0, base, !two);
-              if (n == 1) umma_commit(&bar.q_empty[0]);
-            }
-            if (two && !begun1) {
-              wait(&bar.q_full[1], units1);
-              qk(1, base, true);
-              if (n == 1) umma_commit(&bar.q_empty[1]);
-            }
-            begun0 = begun1 = false;
             const bool more = next(w, u);
             const bool two_next = more && u.rows > kRows;
+            bool out0 = false, out1 = false;  // the next unit's first products are out
+            // Step j of stream s, then the stream's next product: of this unit, or
+            // the first of the next one (before the first step: this unit's first,
+            // where the unit before did not leave it behind).
 #pragma unroll 1
-            for (int e = 0; ok && e < 2 * n; ++e) {
-              // Step j of stream s, and the stream's next product behind it: of
-              // this unit, or the first of the next one.
+            for (int e = -2; ok && e < 2 * n; ++e) {
               const int j = e >> 1, s = e & 1;
               if (s && !two) continue;
-              pv(s, base + j, s ? count1 : count0, j == 0, s ? units1 : units, s || !two);
-              if (s) ++count1; else ++count0;
-              if (!ok) break;
-              const bool last = j + 1 == n;
-              if (last) umma_commit(&bar.o_full[s]);
-              if (last && !(s ? two_next : more)) continue;
-              if (last) {
-                wait(&bar.q_full[s], (s ? units1 : units) + 1);
-                if (s) begun1 = true; else begun0 = true;
+              if (j < 0 && (s ? begun1 : begun0)) continue;
+              const int behind = s ? units1 : units;
+              if (j >= 0) {
+                pv(s, base + j, s ? count1 : count0, j == 0, behind, s || !two);
+                if (s) ++count1; else ++count0;
               }
+              const bool last = j + 1 == n;
+              if (last) commit(&bar.o_full[s]);
+              if (last && !(s ? two_next : more)) continue;
+              if (last || j < 0) wait(&bar.q_full[s], behind + (last ? 1 : 0));
               qk(s, base + j + 1, s || !(last ? two_next : two));
-              if (last ? u.n == 1 : j + 2 == n) umma_commit(&bar.q_empty[s]);
+              if (last ? u.n == 1 : j + 2 == n) commit(&bar.q_empty[s]);
+              if (last && s) out1 = true;
+              if (last && !s) out0 = true;
             }
+            begun0 = out0;
+            begun1 = out1;
             ++units;
             if (two) ++units1;
             base += n;
@@ -365,11 +373,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (i >= 0) {
                 pv(s, base + i, s ? count1 : count0, i < 2, s ? units1 : units, true);
                 if (s) ++count1; else ++count0;
-                if (i + 2 >= u.n) umma_commit(&bar.o_full[s]);
+                if (i + 2 >= u.n) commit(&bar.o_full[s]);
               }
               if (ok && i + 2 < u.n) {
                 qk(s, base + i + 2, true);
-                if (i + 3 == u.n) umma_commit(&bar.q_empty[0]);
+                if (i + 3 == u.n) commit(&bar.q_empty[0]);
               }
             }
             ++units;
@@ -377,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             base += u.n;
           }
         }
-        umma_commit(&bar.drain);
+        commit(&bar.drain);
         drain_wait(&bar.drain, 0u);
       }
       __syncwarp();
@@ -492,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
     // ---------------------------------------------------------- softmax
     const int s = warp >> 2;
     const uint32_t t_s = tmem + s * kKeys + quad, t_o = tmem + 256 + s * 128 + quad;
@@ -585,11 +593,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++done;
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
     // ---------------------------------------------------------- rows
     // A warp keeps to the 32 rows of its TMEM lanes (of each tile) throughout, so
     // its pieces of Q, scores and staging need no barrier beyond the warp.
-    uint8_t* my_stage = stage + quarter * 32 * 128;
+    uint8_t* my_stage = stage + quarter * 32 * 64;
     const int my0 = quarter * 32;  // first of the warp's rows in a tile
     int done0 = 0, done1 = 0;      // units behind, of each stream
     bool ok = true;
@@ -611,10 +619,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto row_base = [&](const Unit& u, int64_t row_stride) {
       return (static_cast<int64_t>(u.r) * a.B + beam_of(u.row0)) * row_stride + u.g * a.G * D;
     };
-    // Row of [level][R * B][Hkv][D] for slot 0 of the unit's request and key head.
-    auto beam_base = [&](const Unit& u, int v) {
-      return ((static_cast<int64_t>(v) * a.R + u.r) * a.B * a.Hkv + u.g) * D;
+    // 16-byte word of [level][R * B][Hkv][D] where slot 0 of the unit's request and
+    // key head begins at level 0, and words from a slot to the next.
+    auto beam_base = [&](const Unit& u) {
+      return static_cast<uint32_t>((static_cast<int64_t>(u.r) * a.B * a.Hkv + u.g) * (D / 8));
     };
+    const uint32_t slot16 = static_cast<uint32_t>(a.Hkv * (D / 8));
 
     // Q of unit u into its tiles, behind the last product with the ones before.
     // (`more0`, `more1`: the unit before, not yet counted, used the stream.)
@@ -635,9 +645,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t at = __shfl_sync(0xFFFFFFFFu, off, lr);
           if (lr < valid) cp_async16(qt + unit_at(my0 + lr, c), src + at);
         }
-        cp_async_wait();
-        __syncwarp();
+      }
+      cp_async_wait();
+      __syncwarp();
+#pragma unroll 1
+      for (int t = 0; t < P::kTiles; ++t) {
         if (a.q_flip) {
+          uint8_t* qt = smem + t * P::kTile;
 #pragma unroll 1
           for (int e = lane; e < 32 * kUnits; e += 32) {
             uint4* q = reinterpret_cast<uint4*>(qt + unit_at(my0 + e / kUnits, e % kUnits));
@@ -669,14 +683,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int t = 0; t < P::kTiles; ++t) at[t] = p[t] < 0 || (v > 0 && p[t] >= a.B) ? -1 : p[t];
       }
+      __syncwarp();
+      // Dead rows (and those past the last) take a live row's slots, so that what
+      // is loaded for them is a live beam's; their weights are zero.
       uint32_t dead = 0u;
 #pragma unroll
-      for (int t = 0; t < P::kTiles; ++t)
+      for (int t = 0; t < P::kTiles; ++t) {
+        const uint32_t live = __ballot_sync(0xFFFFFFFFu, at[t] >= 0);
         if (at[t] < 0) {
           dead |= 1u << t;
+          uint16_t* tab = slots + (t * kRows + my0) * P::kLevels;
+#pragma unroll 1
           for (int v = 0; v < a.level; ++v)
-            slots[(t * kRows + my0 + lane) * P::kLevels + v] = kNoSlot;
+            tab[lane * P::kLevels + v] = live ? tab[(__ffs(live) - 1) * P::kLevels + v] : 0;
         }
+      }
       __syncwarp();
       return dead;
     };
@@ -697,48 +718,50 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int i0 = u.row0 + tile * kRows + my0;
       const int c = lane & 3, n8 = lane >> 2;
       const uint8_t* qt = smem + tile * P::kTile;
-      const int64_t key_stride = static_cast<int64_t>(a.Hkv) * D;
+      const uint4* kb16 = reinterpret_cast<const uint4*>(a.kb);
+      const uint4* vb16 = reinterpret_cast<const uint4*>(a.vb);
+      const uint32_t base16 = beam_base(u);
       // ---- scores
 #pragma unroll 1
       for (int rg = 0; rg < valid; rg += 16) {
         constexpr int kWords = D / 32;  // 16-byte words of a lane's quarter of D
         const int b0 = beam_of(i0 + rg), b_end = beam_of(i0 + min(rg + 15, valid - 1));
         const int j_lo = beam_of(i0 + rg + n8) - b0, j_hi = beam_of(i0 + rg + n8 + 8) - b0;
+        uint4 qa[kWords], qb[kWords];
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) {
+          qa[k] = *reinterpret_cast<const uint4*>(qt + unit_at(my0 + rg + n8, c * kWords + k));
+          qb[k] = *reinterpret_cast<const uint4*>(qt + unit_at(my0 + rg + n8 + 8, c * kWords + k));
+        }
 #pragma unroll 1
         for (int n0 = 0; n0 <= b_end - b0; n0 += 8) {
-          // This lane's key: beam b0 + n0 + n8, through its first row in the group.
-          const int kb = b0 + n0 + n8;
-          const uint16_t* of = tab + max(rg, kb * a.G - i0) * P::kLevels;
+          // This lane's key: beam b0 + n0 + n8 (or the last one, again), through
+          // its first row in the group.
+          const uint16_t* of =
+              tab + max(rg, min(b0 + n0 + n8, b_end) * a.G - i0) * P::kLevels;
+          const int lo = j_lo - n0, hi = j_hi - n0;
 #pragma unroll 1
-          for (int v0 = 0; v0 < a.level; v0 += 4) {  // four levels' loads in flight
-            uint4 kw[4][kWords];
+          for (int v0 = 0; v0 < a.level; v0 += 2) {  // two levels' loads in flight
+            uint4 kw[2][kWords];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint16_t slot = kb <= b_end && v0 + e < a.level ? of[v0 + e] : kNoSlot;
-              const uint4* src = reinterpret_cast<const uint4*>(
-                  a.kb + beam_base(u, v0 + e) + slot * key_stride + c * (D / 4));
+            for (int e = 0; e < 2; ++e) {
+              const int v = min(v0 + e, a.level - 1);
+              const uint4* src =
+                  kb16 + (base16 + v * a.level16 + of[v] * slot16 + c * static_cast<uint32_t>(kWords));
 #pragma unroll
-              for (int k = 0; k < kWords; ++k) {
-                kw[e][k] = make_uint4(0u, 0u, 0u, 0u);
-                if (slot != kNoSlot) kw[e][k] = src[k];
-              }
+              for (int k = 0; k < kWords; ++k) kw[e][k] = src[k];
             }
-            float z[4][4] = {};
+            float z[2][4] = {};
 #pragma unroll
             for (int k = 0; k < kWords; ++k) {
-              const uint4 qa =
-                  *reinterpret_cast<const uint4*>(qt + unit_at(my0 + rg + n8, c * kWords + k));
-              const uint4 qb =
-                  *reinterpret_cast<const uint4*>(qt + unit_at(my0 + rg + n8 + 8, c * kWords + k));
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                mma_16816(z[e], qa.x, qb.x, qa.y, qb.y, kw[e][k].x, kw[e][k].y);
-                mma_16816(z[e], qa.z, qb.z, qa.w, qb.w, kw[e][k].z, kw[e][k].w);
+              for (int e = 0; e < 2; ++e) {
+                mma_16816(z[e], qa[k].x, qb[k].x, qa[k].y, qb[k].y, kw[e][k].x, kw[e][k].y);
+                mma_16816(z[e], qa[k].z, qb[k].z, qa[k].w, qb[k].w, kw[e][k].z, kw[e][k].w);
               }
             }
-            const int lo = j_lo - n0, hi = j_hi - n0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 2; ++e) {
               if (v0 + e < a.level) {
                 if ((lo >> 1) == c)
                   xs[(rg + n8) * P::kLevels + v0 + e] = (lo & 1 ? z[e][1] : z[e][0]) * a.scale_log2;
@@ -764,48 +787,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-      // ---- values
+      // ---- values, 16 rows by 64 columns at a time
       const uint32_t off = row_off(u, tile, a.out_stride);
       __nv_bfloat16* out = a.out + row_base(u, a.out_stride);
 #pragma unroll 1
-      for (int rg = 0; rg < valid; rg += 16) {
-        constexpr int kCols = D / 8;         // columns a lane reads of a key; n blocks
-        constexpr int kWords = kCols / 2;    // their 32-bit words
-        float y[kCols][4];
-#pragma unroll
-        for (int k = 0; k < kCols; ++k)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) y[k][e] = 0.f;
+      for (int part = 0; part < 2 * (D / 64); ++part) {
+        const int rg = part / (D / 64) * 16, d0 = part % (D / 64) * 64;
+        if (rg >= valid) break;
+        float y[8][4] = {};
         const int b0 = beam_of(i0 + rg), b_end = beam_of(i0 + min(rg + 15, valid - 1));
         const int j_lo = beam_of(i0 + rg + n8) - b0, j_hi = beam_of(i0 + rg + n8 + 8) - b0;
 #pragma unroll 1
         for (int n0 = 0; n0 <= b_end - b0; n0 += 8) {
+          // Keys of this lane: beams b0 + n0 + 2c, + 1 at two levels; columns
+          // d0 + 8 n8 .. + 7 of each.
+          const int kb = b0 + n0 + 2 * c, lo = j_lo - n0, hi = j_hi - n0;
+          const uint16_t* of0 = tab + max(rg, min(kb, b_end) * a.G - i0) * P::kLevels;
+          const uint16_t* of1 = tab + max(rg, min(kb + 1, b_end) * a.G - i0) * P::kLevels;
 #pragma unroll 1
           for (int v0 = 0; v0 < a.level; v0 += 2) {
-            // Keys of this lane: beams b0 + n0 + 2c, + 1 at levels v0, v0 + 1.
-            uint32_t vw[4][kWords];
+            uint4 vw[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int kb = b0 + n0 + 2 * c + (e & 1), v = v0 + (e >> 1);
-              const uint16_t slot = kb <= b_end && v < a.level
-                                        ? tab[max(rg, kb * a.G - i0) * P::kLevels + v]
-                                        : kNoSlot;
-              const uint4* src = reinterpret_cast<const uint4*>(
-                  a.vb + beam_base(u, v) + slot * key_stride + n8 * kCols);
-#pragma unroll
-              for (int k = 0; k < kWords; k += 4) {
-                uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                if (slot != kNoSlot) w = src[k / 4];
-                vw[e][k] = w.x;
-                vw[e][k + 1] = w.y;
-                vw[e][k + 2] = w.z;
-                vw[e][k + 3] = w.w;
-              }
+              const int v = min(v0 + (e >> 1), a.level - 1);
+              vw[e] = vb16[base16 + v * a.level16 + (e & 1 ? of1 : of0)[v] * slot16 +
+                           static_cast<uint32_t>(d0 / 8 + n8)];
             }
             // Weights: a row's in the place of its own beam, as the sum of two bf16
             // (its values are rounded once on their way through the output, and
             // that takes what rounding the weights are allowed).
-            const int lo = j_lo - n0, hi = j_hi - n0;
             uint32_t aw[4], ar[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -817,57 +827,56 @@ __global__ void __launch_bounds__(kThreads, 1)
               aw[e] = at & 1 ? bf16x2(0.f, head) : bf16x2(head, 0.f);
               ar[e] = at & 1 ? bf16x2(0.f, wt - head) : bf16x2(wt - head, 0.f);
             }
+            const uint32_t w[4][4] = {{vw[0].x, vw[0].y, vw[0].z, vw[0].w},
+                                      {vw[1].x, vw[1].y, vw[1].z, vw[1].w},
+                                      {vw[2].x, vw[2].y, vw[2].z, vw[2].w},
+                                      {vw[3].x, vw[3].y, vw[3].z, vw[3].w}};
 #pragma unroll
-            for (int k = 0; k < kWords; ++k) {
-              const uint32_t e0 = __byte_perm(vw[0][k], vw[1][k], 0x5410);
-              const uint32_t e1 = __byte_perm(vw[2][k], vw[3][k], 0x5410);
-              const uint32_t o0 = __byte_perm(vw[0][k], vw[1][k], 0x7632);
-              const uint32_t o1 = __byte_perm(vw[2][k], vw[3][k], 0x7632);
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t e0 = __byte_perm(w[0][k], w[1][k], 0x5410);
+              const uint32_t e1 = __byte_perm(w[2][k], w[3][k], 0x5410);
+              const uint32_t o0 = __byte_perm(w[0][k], w[1][k], 0x7632);
+              const uint32_t o1 = __byte_perm(w[2][k], w[3][k], 0x7632);
               mma_16816(y[2 * k], aw[0], aw[1], aw[2], aw[3], e0, e1);
-              mma_16816(y[2 * k], ar[0], ar[1], ar[2], ar[3], e0, e1);
               mma_16816(y[2 * k + 1], aw[0], aw[1], aw[2], aw[3], o0, o1);
+              mma_16816(y[2 * k], ar[0], ar[1], ar[2], ar[3], e0, e1);
               mma_16816(y[2 * k + 1], ar[0], ar[1], ar[2], ar[3], o0, o1);
             }
           }
         }
         // An infinity or NaN in one beam's values would reach its neighbours
-        // through their zero weights: such a group is added up row by row.
+        // through their zero weights: such a part is added up row by row.
         float all = 0.f;
 #pragma unroll
-        for (int k = 0; k < kCols; ++k) all += (y[k][0] + y[k][1]) + (y[k][2] + y[k][3]);
+        for (int k = 0; k < 8; ++k) all += (y[k][0] + y[k][1]) + (y[k][2] + y[k][3]);
         if (__any_sync(0xFFFFFFFFu, !(fabsf(all) < 3.0e38f))) {
 #pragma unroll 1
           for (int lr = rg; lr < min(rg + 16, valid); ++lr) {
             const uint32_t at = __shfl_sync(0xFFFFFFFFu, off, lr);
 #pragma unroll 1
-            for (int d = lane; d < D; d += 32) {
+            for (int d = d0 + lane; d < d0 + 64; d += 32) {
               float z = 0.f;
+#pragma unroll 1
               for (int v = 0; v < a.level; ++v) {
-                const uint16_t slot = tab[lr * P::kLevels + v];
-                if (slot != kNoSlot)
-                  z = fmaf(xs[lr * P::kLevels + v],
-                           __bfloat162float(a.vb[beam_base(u, v) + slot * key_stride + d]), z);
+                const int64_t at16 = base16 + v * a.level16 + tab[lr * P::kLevels + v] * slot16;
+                const float wt = xs[lr * P::kLevels + v];
+                if (wt > 0.f) z = fmaf(wt, __bfloat162float(a.vb[at16 * 8 + d]), z);
               }
               out[at + d] = __float2bfloat16(z);
             }
           }
         } else {
-          // This lane: D / 4 consecutive columns of rows rg + n8 and + 8.
+          // This lane: columns d0 + 16 c .. + 15 of rows rg + n8 and + 8.
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            const int lr = rg + n8 + half * 8;
+            const int lr = rg + n8 + half * 8, e = half * 2;
             const uint32_t at = __shfl_sync(0xFFFFFFFFu, off, lr);
             if (lr < valid) {
-              uint4* dst = reinterpret_cast<uint4*>(out + at + c * (D / 4));
-#pragma unroll
-              for (int q = 0; q < 2; ++q)  // columns of n = 2c, then of n = 2c + 1
-#pragma unroll
-                for (int k = 0; k < kCols; k += 8) {
-                  const int e = half * 2 + q;
-                  dst[(q * kCols + k) / 8] =
-                      make_uint4(bf16x2(y[k][e], y[k + 1][e]), bf16x2(y[k + 2][e], y[k + 3][e]),
-                                 bf16x2(y[k + 4][e], y[k + 5][e]), bf16x2(y[k + 6][e], y[k + 7][e]));
-                }
+              uint4* dst = reinterpret_cast<uint4*>(out + at + d0 + c * 16);
+              dst[0] = make_uint4(bf16x2(y[0][e], y[1][e]), bf16x2(y[2][e], y[3][e]),
+                                  bf16x2(y[4][e], y[5][e]), bf16x2(y[6][e], y[7][e]));
+              dst[1] = make_uint4(bf16x2(y[0][e + 1], y[1][e + 1]), bf16x2(y[2][e + 1], y[3][e + 1]),
+                                  bf16x2(y[4][e + 1], y[5][e + 1]), bf16x2(y[6][e + 1], y[7][e + 1]));
             }
           }
         }
@@ -930,25 +939,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         part[D] = top;
         part[D + 1] = total;
       }
-      uint32_t packed[D / 2];
       const int sa = kDual ? tile : 0;
-#pragma unroll
+      const bool read_a = valid > 0 && steps_of<kDual>(u, sa) > 0;
+      const bool read_b = !kDual && valid > 0 && steps_of<kDual>(u, 1) > 0;
+      const int u4 = lane & 3;
+#pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         float o[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = 0.f;
-        if (valid > 0 && steps_of<kDual>(u, sa) > 0) {
+        if (read_a) {
           uint32_t v[32];
           tmem_ld32(tmem + 256 + sa * 128 + quad + c, v);
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = has_a ? __uint_as_float(v[e]) * f0 : 0.f;
         }
-        if (!kDual && valid > 0 && steps_of<kDual>(u, 1) > 0) {
+        if (read_b) {
           uint32_t v[32];
           tmem_ld32(tmem + 256 + 128 + quad + c, v);
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (has_b) o[e] = fmaf(__uint_as_float(v[e]), f1, o[e]);
+        }
+        if (c + 32 == D) {  // O has been read
+          tc_fence_before();
+          __syncwarp();
+#pragma unroll 1
+          for (int s = kDual ? tile : 0; s < s_end; ++s)
+            if (steps_of<kDual>(u, s) > 0) {
+              if (lane == 0) mbar_arrive(&bar.o_empty[s]);
+              if (s) ++done1; else ++done0;
+            }
         }
         if (fp > 0.f && lane < valid) {
 #pragma unroll
@@ -963,40 +984,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 4; ++k) o[e + 4 + k] = fmaf(fp, f[k], o[e + 4 + k]);
           }
         }
-        if (a.split > 1 && valid > 0) {
+        if (a.split > 1) {
+          if (valid > 0) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(part + c + e) =
-                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4*>(part + c + e) =
+                  make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
+          continue;
         }
+        // From a row per lane to 64-byte pieces of rows.
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) packed[(c + e) / 2] = bf16x2(o[e], o[e + 1]);
-      }
-      // O has been read.
-      tc_fence_before();
-      __syncwarp();
-      for (int s = kDual ? tile : 0; s < s_end; ++s)
-        if (steps_of<kDual>(u, s) > 0) {
-          if (lane == 0) mbar_arrive(&bar.o_empty[s]);
-          if (s) ++done1; else ++done0;
-        }
-      if (a.split > 1 || valid <= 0) return;
-      // From a row per lane to whole 128-byte lines of the output.
-      const int u8 = lane & 7;
-#pragma unroll
-      for (int c = 0; c < D; c += 64) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          *reinterpret_cast<uint4*>(my_stage + lane * 128 + (((k ^ lane) & 7) << 4)) =
-              make_uint4(packed[c / 2 + k * 4], packed[c / 2 + k * 4 + 1],
-                         packed[c / 2 + k * 4 + 2], packed[c / 2 + k * 4 + 3]);
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<uint4*>(my_stage + lane * 64 + ((k ^ (lane >> 1)) & 3) * 16) =
+              make_uint4(bf16x2(o[k * 8], o[k * 8 + 1]), bf16x2(o[k * 8 + 2], o[k * 8 + 3]),
+                         bf16x2(o[k * 8 + 4], o[k * 8 + 5]), bf16x2(o[k * 8 + 6], o[k * 8 + 7]));
         __syncwarp();
-#pragma unroll 4
-        for (int lr = lane >> 3; lr < 32; lr += 4) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int lr = q * 8 + (lane >> 2);
           const uint32_t at = __shfl_sync(0xFFFFFFFFu, off, lr);
-          const uint4 w =
-              *reinterpret_cast<const uint4*>(my_stage + lr * 128 + (((u8 ^ lr) & 7) << 4));
-          if (lr < valid) *reinterpret_cast<uint4*>(out + at + c + u8 * 8) = w;
+          const uint4 w = *reinterpret_cast<const uint4*>(my_stage + lr * 64 +
+                                                          ((u4 ^ (lr >> 1)) & 3) * 16);
+          if (lr < valid) *reinterpret_cast<uint4*>(out + at + c + u4 * 8) = w;
         }
         __syncwarp();
       }
@@ -1209,6 +1219,8 @@ extern "C" int beam_attention(const void* q, int64_t q_row_stride, const void* k
     return set_error(SIDBEAM_ERR_INVALID_ARG, "beam_attention: a stride is smaller than its row");
   if (q_row_stride >= 1 << 24 || out_row_stride >= 1 << 24)
     return set_error(SIDBEAM_ERR_INVALID_ARG, "beam_attention: a row stride is 2^24 or more");
+  if (static_cast<int64_t>(R) * B * Hkv * (D / 8) * std::max(level, 1) > 0xFFFFFFFFll)
+    return set_error(SIDBEAM_ERR_INVALID_ARG, "beam_attention: k_beam of 64 GiB or more");
   if (page_stride > (1ll << 38))
     return set_error(SIDBEAM_ERR_INVALID_ARG, "beam_attention: page_stride too large");
   if (misaligned(q, 16) || misaligned(k_cache, 16) || misaligned(v_cache, 16) ||
@@ -1244,6 +1256,7 @@ extern "C" int beam_attention(const void* q, int64_t q_row_stride, const void* k
   a.scale_log2 = std::max(fabsf(scale) * kLog2e, 1e-30f);
   a.q_flip = scale < 0.f ? 0x80008000u : 0u;
   a.G = H / Hkv;
+  a.level16 = static_cast<uint32_t>(static_cast<int64_t>(R) * B * Hkv * (D / 8));
   a.page_log2 = 0;
   while (page_table && (1 << a.page_log2) < page_size) ++a.page_log2;
   a.g_magic = a.G > 1 ? static_cast<uint32_t>((0x100000000ull + a.G - 1) / a.G) : 0u;

@@ -25,20 +25,22 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
          (static_cast<uint64_t>(2) << 61);
 }
 
-// Waits for a barrier's phase number `phase` (its parity), with the limits of
-// bounded_wait in fewer instructions: these kernels run several roles at once, and
-// their speed depends on all of their loops staying in the instruction cache. (Out
-// of line it costs more: with a call in the kernel the compiler keeps every role to
-// the registers of the launch, whatever setmaxnreg gives it.)
+// Waits for a barrier's phase number `phase` (its parity), as bounded_wait in far
+// fewer instructions: kernels that run several roles at once depend on all of their
+// loops staying in the instruction cache. The limit is a number of looks, each of
+// which the hardware may stretch to kSuspendHintNs: a tenth of a second to some
+// seconds, against waits of at most milliseconds. (Out of line it costs more: with
+// a call in the kernel the compiler keeps every role to the registers of the
+// launch, whatever setmaxnreg gives it.)
+constexpr int kWaitLooks = 1 << 22;
 // One thread:
 __device__ __forceinline__ bool lane_wait(uint64_t* bar, uint32_t phase, volatile int* abort,
                                           uint32_t* status) {
-  uint64_t begun = 0;
+  int looks = 0;
+#pragma unroll 1
   while (!mbar_try_wait(bar, phase & 1u)) {
     if (*abort) return false;
-    const uint64_t now = global_timer_ns();
-    if (begun == 0) begun = now;
-    if (now - begun > kWaitTimeoutNs) {
+    if (++looks == kWaitLooks) {
       *abort = 1;
       atomicOr(status, kStatusTimeout);
       return false;
