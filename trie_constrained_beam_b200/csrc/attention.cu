@@ -197,7 +197,10 @@ __device__ __forceinline__ int tile_of(int s, int j) {
 __device__ __forceinline__ int pos_k(int t, int ahead) { return t < ahead ? t : 2 * t - ahead + 1; }
 __device__ __forceinline__ int pos_v(int t, int ahead) { return 2 * t + ahead; }
 
-template <int D, bool kDual>
+// kPath: the rows have ancestors; kSplit: units are split over clusters. (Flags of
+// the instance, since every part that a kernel does not have is room in the
+// instruction cache: 128 KB of code measured 15-20% slower than 96 KB.)
+template <int D, bool kDual, bool kPath, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v,
@@ -215,9 +218,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int rank = a.split > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int first_unit = static_cast<int>(blockIdx.x) / a.split;
-  const int stride = a.split > 1 ? a.units : static_cast<int>(gridDim.x);
+  const int rank = kSplit ? static_cast<int>(cluster_rank()) : 0;
+  const int first_unit = static_cast<int>(blockIdx.x) >> a.split_log2;
+  const int stride = kSplit ? a.units : static_cast<int>(gridDim.x);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 8; ++s) {
@@ -257,57 +260,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the tensor core, at the same time: measured 13% slower. And where it saw
       // only its stream's slots it could take an older phase of a slot for the one
       // it waits for: a wait tells phases apart by parity alone.)
-      // The warp goes together and one lane issues: what is the same for all
-      // lanes can then live in uniform registers, where the instruction wants it.
-      {
+      // What stands between a step's weights and the next scores is on the path
+      // of every step, so a step's other waits (its V, the next K) come first, and
+      // its two products are issued back to back.
+      if (elect_one()) {
         bool ok = true;
         auto wait = [&](uint64_t* b, int phase) {
-          ok = ok && warp_wait(b, static_cast<uint32_t>(phase), &bar.abort, a.status);
+          ok = ok && lane_wait(b, static_cast<uint32_t>(phase), &bar.abort, a.status);
         };
-        auto commit = [&](uint64_t* b) {
-          if (elect_one()) umma_commit(b);
-          __syncwarp();
-        };
+        auto wait_load = [&](int pos) { wait(&bar.full[pos % P::kSlots], pos / P::kSlots); };
         const uint32_t ring_at = smem_addr(ring);
         const uint64_t q0 = smem_desc(smem_addr(smem));
-        // S of stream s from key tile t (counted over the CTA's units).
-        // `free`: the ring slot has no other user to come.
-        auto qk = [&](int s, int t, bool free) {
-          const int pos = pos_k(t, P::kAhead), slot = pos % P::kSlots;
-          wait(&bar.full[slot], pos / P::kSlots);
-          if (!ok) return;
-          tc_fence_after();
-          const uint64_t k = smem_desc(ring_at + slot * P::kTile);
+        // S of stream s from the K tile at a position of the ring.
+        auto qk = [&](int s, int pos) {
+          const uint64_t k = smem_desc(ring_at + (pos % P::kSlots) * P::kTile);
           const uint64_t q = q0 + (kDual && s ? P::kTile >> 4 : 0);
-          if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = ((kk >> 2) * P::kHalf + (kk & 3) * 32) >> 4;
-              umma_f16(tmem + s * kKeys, q + off, k + off, kIdescQK, kk > 0 ? 1u : 0u);
-            }
-            umma_commit(&bar.s_full[s]);
-            if (free) umma_commit(&bar.empty[slot]);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * P::kHalf + (kk & 3) * 32) >> 4;
+            umma_f16(tmem + s * kKeys, q + off, k + off, kIdescQK, kk > 0 ? 1u : 0u);
           }
-          __syncwarp();
+          umma_commit(&bar.s_full[s]);
         };
-        // O of stream s += P V of key tile t, once step `count`'s weights are there.
-        auto pv = [&](int s, int t, int count, bool first, int done, bool free) {
-          const int pos = pos_v(t, P::kAhead), slot = pos % P::kSlots;
-          const uint64_t v = smem_desc_mn(ring_at + slot * P::kTile, P::kHalf);
-          wait(&bar.full[slot], pos / P::kSlots);
-          if (first && done > 0) wait(&bar.o_empty[s], done - 1);
-          wait(&bar.p_ready[s], count);
-          if (!ok) return;
-          tc_fence_after();
-          if (elect_one()) {
+        // O of stream s += P V with the V tile at a position of the ring.
+        auto pv = [&](int s, int pos, bool first) {
+          const uint64_t v = smem_desc_mn(ring_at + (pos % P::kSlots) * P::kTile, P::kHalf);
 #pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk)
-              umma_f16_ts(tmem + 256 + s * 128, tmem + s * kKeys + kk * 8, v + kk * (2048 >> 4),
-                          idesc_pv(D), kk > 0 || !first ? 1u : 0u);
-            if (free) umma_commit(&bar.empty[slot]);
-          }
-          __syncwarp();
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            umma_f16_ts(tmem + 256 + s * 128, tmem + s * kKeys + kk * 8, v + kk * (2048 >> 4),
+                        idesc_pv(D), kk > 0 || !first ? 1u : 0u);
         };
+        auto free_slot = [&](int pos) { umma_commit(&bar.empty[pos % P::kSlots]); };
         int base = 0, units = 0, units1 = 0;  // tiles and units behind (of stream 1)
         int count0 = 0, count1 = 0;           // steps behind, of each stream
         if constexpr (kDual) {
@@ -324,37 +307,52 @@ __global__ void __launch_bounds__(kThreads, 1)
           int w = first_unit;
           Unit u;
           bool have = next(w, u);
-          bool begun0 = false, begun1 = false;  // the unit's first products are out
+          bool out0 = false, out1 = false;  // the unit's first products are out
           while (ok && have) {
             const bool two = u.rows > kRows;
             const int n = u.n;
             const bool more = next(w, u);
             const bool two_next = more && u.rows > kRows;
-            bool out0 = false, out1 = false;  // the next unit's first products are out
+            const bool begun0 = out0, begun1 = out1;
+            out0 = out1 = false;
             // Step j of stream s, then the stream's next product: of this unit, or
-            // the first of the next one (before the first step: this unit's first,
-            // where the unit before did not leave it behind).
+            // the first of the next one (before step 0: this unit's first, where
+            // the unit before did not leave it behind).
 #pragma unroll 1
             for (int e = -2; ok && e < 2 * n; ++e) {
               const int j = e >> 1, s = e & 1;
               if (s && !two) continue;
               if (j < 0 && (s ? begun1 : begun0)) continue;
               const int behind = s ? units1 : units;
-              if (j >= 0) {
-                pv(s, base + j, s ? count1 : count0, j == 0, behind, s || !two);
-                if (s) ++count1; else ++count0;
+              const bool last = j + 1 == n, closing = s || !two;
+              const int vp = pos_v(base + j, 1), kp = pos_k(base + j + 1, 1);
+              if (!last) {
+                if (j < 0) wait(&bar.q_full[s], behind);
+                wait_load(kp);
               }
-              const bool last = j + 1 == n;
-              if (last) commit(&bar.o_full[s]);
-              if (last && !(s ? two_next : more)) continue;
-              if (last || j < 0) wait(&bar.q_full[s], behind + (last ? 1 : 0));
-              qk(s, base + j + 1, s || !(last ? two_next : two));
-              if (last ? u.n == 1 : j + 2 == n) commit(&bar.q_empty[s]);
-              if (last && s) out1 = true;
-              if (last && !s) out0 = true;
+              if (j >= 0) {
+                wait_load(vp);
+                if (j == 0 && behind > 0) wait(&bar.o_empty[s], behind - 1);
+                wait(&bar.p_ready[s], s ? count1++ : count0++);
+                if (!ok) break;
+                tc_fence_after();
+                pv(s, vp, j == 0);
+              }
+              if (last) {
+                umma_commit(&bar.o_full[s]);
+                if (closing) free_slot(vp);
+                if (!(s ? two_next : more)) continue;
+                wait(&bar.q_full[s], behind + 1);
+                wait_load(kp);
+                if (s) out1 = true; else out0 = true;
+              }
+              if (!ok) break;
+              tc_fence_after();
+              qk(s, kp);
+              if (last ? s || !two_next : closing) free_slot(kp);
+              if (last ? u.n == 1 : j + 2 == n) umma_commit(&bar.q_empty[s]);
+              if (j >= 0 && !last && closing) free_slot(vp);
             }
-            begun0 = out0;
-            begun1 = out1;
             ++units;
             if (two) ++units1;
             base += n;
@@ -370,22 +368,32 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int i = -2; ok && i < u.n; ++i) {
               const int s = i & 1;
+              const int vp = pos_v(base + i, 2), kp = pos_k(base + i + 2, 2);
+              if (i >= 0) wait_load(vp);
+              if (i + 2 < u.n) wait_load(kp);
               if (i >= 0) {
-                pv(s, base + i, s ? count1 : count0, i < 2, s ? units1 : units, true);
-                if (s) ++count1; else ++count0;
-                if (i + 2 >= u.n) commit(&bar.o_full[s]);
+                const int behind = s ? units1 : units;
+                if (i < 2 && behind > 0) wait(&bar.o_empty[s], behind - 1);
+                wait(&bar.p_ready[s], s ? count1++ : count0++);
               }
-              if (ok && i + 2 < u.n) {
-                qk(s, base + i + 2, true);
-                if (i + 3 == u.n) commit(&bar.q_empty[0]);
+              if (!ok) break;
+              tc_fence_after();
+              if (i >= 0) pv(s, vp, i < 2);
+              if (i + 2 < u.n) {
+                qk(s, kp);
+                free_slot(kp);
+                if (i + 3 == u.n) umma_commit(&bar.q_empty[0]);
+              } else if (i >= 0) {
+                umma_commit(&bar.o_full[s]);
               }
+              if (i >= 0) free_slot(vp);
             }
             ++units;
             if (u.n > 1) ++units1;
             base += u.n;
           }
         }
-        commit(&bar.drain);
+        umma_commit(&bar.drain);
         drain_wait(&bar.drain, 0u);
       }
       __syncwarp();
@@ -513,7 +521,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (steps == 0) continue;
       const int tile_rows = kDual && s == 1 ? u.rows - kRows : min(u.rows, kRows);
       const bool active = quarter * 32 < tile_rows;
-      float m = kNegInf, l = 0.f;
+      // A row's weights are 2^(x - m) for a reference m that follows the row's
+      // maximum. A tile is weighed in two halves, so that only a half's maximum
+      // stands before its weights; m moves (with O and l) before the first half
+      // once it is behind by 2^kNear, before the second only if it is behind by
+      // 2^kFar (the first half's weights then move too), far below any overflow.
+      constexpr float kNear = 8.f, kFar = 60.f;
+      float m = kNegInf, l = 0.f, seen = kNegInf;  // seen: the maximum so far
       for (int j = 0; j < steps; ++j, ++count) {
         if (!warp_wait(&bar.s_full[s], count, &bar.abort, a.status)) {
           ok = false;
@@ -521,64 +535,82 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         if (active) {
-          float x[kKeys];
-#pragma unroll
-          for (int c = 0; c < kKeys; c += 32)
-            tmem_ld32_async(t_s + c, reinterpret_cast<uint32_t*>(x) + c);
-          tmem_wait_ld();
-          if (u.ragged && tile_of<kDual>(s, j) == u.n - 1) {
-#pragma unroll
-            for (int e = 0; e < kKeys; ++e)
-              if (e >= u.ragged) x[e] = kNegInf;
-          }
-          float t4[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) t4[e] = fmaxf(x[e], x[e + 4]);
-#pragma unroll
-          for (int e = 8; e < kKeys; e += 8) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) t4[k] = fmaxf(fmaxf(t4[k], x[e + k]), x[e + 4 + k]);
-          }
-          const float t = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * sc;
-          // The reference m moves only when a row's maximum passes it by 2^8:
-          // smaller growth keeps the weights below 2^8 and spares the pass over O.
-          if (j == 0) {
-            m = t;
-          } else if (const bool grow = t > m + 8.f; __any_sync(0xFFFFFFFFu, grow)) {
-            // A row that need not move keeps its reference, so that no row's
-            // result depends on its neighbours.
-            const float f = grow ? ex2_approx(m - t) : 1.f;
-            l *= f;
-            m = grow ? t : m;
+          const int last = u.ragged && tile_of<kDual>(s, j) == u.n - 1 ? u.ragged : kKeys;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-              uint32_t o[16];
-              tmem_ld16(t_o + c, o);
+          for (int h = 0; h < kKeys; h += 64) {
+            float x[64];
+            uint32_t* xr = reinterpret_cast<uint32_t*>(x);
+            tmem_ld32_async(t_s + h, xr);
+            tmem_ld32_async(t_s + h + 32, xr + 32);
+            tmem_wait_ld32(xr);
+            tmem_wait_ld32(xr + 32);
+            if (h + 64 > last) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st16(t_o + c, o);
+              for (int e = 0; e < 64; ++e)
+                if (h + e >= last) x[e] = kNegInf;
             }
-          }
-          const float mref = m > kNegInf ? m : 0.f;
-          const uint64_t sc2 = pack_f32x2(sc, sc), m2 = pack_f32x2(-mref, -mref);
-          uint64_t l2[2] = {pack_f32x2(l, 0.f), pack_f32x2(0.f, 0.f)};
+            float t4[4];
 #pragma unroll
-          for (int c = 0; c < kKeys; c += 32) {
-            uint32_t p[16];
+            for (int e = 0; e < 4; ++e) t4[e] = fmaxf(x[e], x[e + 4]);
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float p0, p1;
-              unpack_f32x2(fma_f32x2(pack_f32x2(x[c + e], x[c + e + 1]), sc2, m2), p0, p1);
-              p0 = ex2_approx(p0);
-              p1 = ex2_approx(p1);
-              l2[(e >> 1) & 1] = add_f32x2(l2[(e >> 1) & 1], pack_f32x2(p0, p1));
-              p[e >> 1] = bf16x2(p0, p1);
+            for (int e = 8; e < 64; e += 8)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) t4[k] = fmaxf(fmaxf(t4[k], x[e + k]), x[e + 4 + k]);
+            seen = fmaxf(seen, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * sc);
+            if (j == 0 && h == 0) {
+              m = seen;
+            } else if (const bool moves = seen > m + (h == 0 ? kNear : kFar);
+                       __any_sync(0xFFFFFFFFu, moves)) {
+              // (A row that need not move keeps its reference, so that no row's
+              // result depends on its neighbours.)
+              const float f = moves ? ex2_approx(m - seen) : 1.f;
+              l *= f;
+              m = moves ? seen : m;
+              if (j > 0) {
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                  uint32_t o[16];
+                  tmem_ld16(t_o + c, o);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                  tmem_st16(t_o + c, o);
+                }
+              }
+              if (h > 0) {  // the first half's weights
+                tmem_wait_st();
+#pragma unroll 1
+                for (int c = 0; c < 32; c += 16) {
+                  uint32_t p[16];
+                  tmem_ld16(t_s + c, p);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e)
+                    p[e] = bf16x2(__uint_as_float(p[e] << 16) * f,
+                                  __uint_as_float(p[e] & 0xFFFF0000u) * f);
+                  tmem_st16(t_s + c, p);
+                }
+              }
             }
-            tmem_st16(t_s + (c >> 1), p);
+            const float mref = m > kNegInf ? m : 0.f;
+            const uint64_t sc2 = pack_f32x2(sc, sc), m2 = pack_f32x2(-mref, -mref);
+            uint64_t l2[2] = {pack_f32x2(l, 0.f), pack_f32x2(0.f, 0.f)};
+#pragma unroll
+            for (int c = 0; c < 64; c += 32) {
+              uint32_t p[16];
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                float p0, p1;
+                unpack_f32x2(fma_f32x2(pack_f32x2(x[c + e], x[c + e + 1]), sc2, m2), p0, p1);
+                p0 = ex2_approx(p0);
+                p1 = ex2_approx(p1);
+                l2[(e >> 1) & 1] = add_f32x2(l2[(e >> 1) & 1], pack_f32x2(p0, p1));
+                p[e >> 1] = bf16x2(p0, p1);
+              }
+              tmem_st16(t_s + ((h + c) >> 1), p);
+            }
+            float la, lb;
+            unpack_f32x2(add_f32x2(l2[0], l2[1]), la, lb);
+            l = la + lb;
           }
-          float la, lb;
-          unpack_f32x2(add_f32x2(l2[0], l2[1]), la, lb);
-          l = la + lb;
           tmem_wait_st();
         }
         tc_fence_before();
@@ -727,12 +759,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kWords = D / 32;  // 16-byte words of a lane's quarter of D
         const int b0 = beam_of(i0 + rg), b_end = beam_of(i0 + min(rg + 15, valid - 1));
         const int j_lo = beam_of(i0 + rg + n8) - b0, j_hi = beam_of(i0 + rg + n8 + 8) - b0;
-        uint4 qa[kWords], qb[kWords];
-#pragma unroll
-        for (int k = 0; k < kWords; ++k) {
-          qa[k] = *reinterpret_cast<const uint4*>(qt + unit_at(my0 + rg + n8, c * kWords + k));
-          qb[k] = *reinterpret_cast<const uint4*>(qt + unit_at(my0 + rg + n8 + 8, c * kWords + k));
-        }
 #pragma unroll 1
         for (int n0 = 0; n0 <= b_end - b0; n0 += 8) {
           // This lane's key: beam b0 + n0 + n8 (or the last one, again), through
@@ -754,10 +780,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             float z[2][4] = {};
 #pragma unroll
             for (int k = 0; k < kWords; ++k) {
+              const uint4 qa =
+                  *reinterpret_cast<const uint4*>(qt + unit_at(my0 + rg + n8, c * kWords + k));
+              const uint4 qb =
+                  *reinterpret_cast<const uint4*>(qt + unit_at(my0 + rg + n8 + 8, c * kWords + k));
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                mma_16816(z[e], qa[k].x, qb[k].x, qa[k].y, qb[k].y, kw[e][k].x, kw[e][k].y);
-                mma_16816(z[e], qa[k].z, qb[k].z, qa[k].w, qb[k].w, kw[e][k].z, kw[e][k].w);
+                mma_16816(z[e], qa.x, qb.x, qa.y, qb.y, kw[e][k].x, kw[e][k].y);
+                mma_16816(z[e], qa.z, qb.z, qa.w, qb.w, kw[e][k].z, kw[e][k].w);
               }
             }
 #pragma unroll
@@ -814,8 +844,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                            static_cast<uint32_t>(d0 / 8 + n8)];
             }
             // Weights: a row's in the place of its own beam, as the sum of two bf16
-            // (its values are rounded once on their way through the output, and
-            // that takes what rounding the weights are allowed).
+            // (its values are rounded once on their way through the output, which
+            // takes what rounding the weights is allowed).
             uint32_t aw[4], ar[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -891,7 +921,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto finish = [&](const Unit& u, int tile, bool dead) {
       const int valid = rows_in(u, tile);
       const int s_end = kDual ? tile + 1 : 2;
-      const bool path = a.level > 0 && rank == 0;
+      const bool path = kPath && rank == 0;
       const uint32_t off = row_off(u, tile, a.out_stride);
       __nv_bfloat16* out = a.out + row_base(u, a.out_stride);
       float mp = kNegInf, lp = 0.f;
@@ -928,23 +958,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       float fp = has_p ? ex2_approx(mp - ref) : 0.f;
       const float sum = f0 * st_a.y + f1 * st_b.y + fp * lp;
       const float total = has_a || has_b || has_p ? sum : 0.f;
-      if (a.split == 1) {
+      if constexpr (!kSplit) {
         const float inv = total > 0.f ? 1.f / total : 0.f;
         f0 *= inv;
         f1 *= inv;
         fp *= inv;
       }
       float* part = reinterpret_cast<float*>(smem) + (tile * kRows + my0 + lane) * P::kPart;
-      if (a.split > 1 && valid > 0) {
+      if (kSplit && valid > 0) {
         part[D] = top;
         part[D + 1] = total;
       }
       const int sa = kDual ? tile : 0;
       const bool read_a = valid > 0 && steps_of<kDual>(u, sa) > 0;
       const bool read_b = !kDual && valid > 0 && steps_of<kDual>(u, 1) > 0;
+      const bool with_path = kPath && fp > 0.f && lane < valid;
       const int u4 = lane & 3;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
+        uint4 pw[4];
+        if (with_path) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) pw[e] = *reinterpret_cast<const uint4*>(out + off + c + e * 8);
+        }
         float o[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = 0.f;
@@ -971,10 +1007,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (s) ++done1; else ++done0;
             }
         }
-        if (fp > 0.f && lane < valid) {
+        if (with_path) {
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
-            const uint4 w = *reinterpret_cast<const uint4*>(out + off + c + e);
+            const uint4 w = pw[e / 8];
             float f[4];
             bf16x4(make_uint2(w.x, w.y), f);
 #pragma unroll
@@ -984,15 +1020,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 4; ++k) o[e + 4 + k] = fmaf(fp, f[k], o[e + 4 + k]);
           }
         }
-        if (a.split > 1) {
+        if constexpr (kSplit) {
           if (valid > 0) {
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
               *reinterpret_cast<float4*>(part + c + e) =
                   make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           }
-          continue;
-        }
+        } else {
         // From a row per lane to 64-byte pieces of rows.
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -1009,6 +1044,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lr < valid) *reinterpret_cast<uint4*>(out + at + c + u4 * 8) = w;
         }
         __syncwarp();
+        }
       }
     };
 
@@ -1019,7 +1055,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int w = first_unit; ok && w < a.units; w += stride) {
       uint32_t dead = 0u;  // bit t: this lane's row of tile t
-      if (a.level > 0) {
+      if (w + stride < a.units) {
+        // The next unit's q on its way to L2.
+        const Unit nx = unit_of<kDual>(a, w + stride, rank);
+#pragma unroll 1
+        for (int t = 0; t < P::kTiles; ++t)
+          if (lane < rows_in(nx, t))
+            for (int c = 0; c < D; c += 64)
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(a.q + row_base(nx, a.q_stride) +
+                                                            row_off(nx, t, a.q_stride) + c));
+      }
+      if constexpr (kPath) {
         dead = walk_path(u);
 #pragma unroll 1
         for (int t = 0; rank == 0 && t * kRows < u.rows; ++t)
@@ -1032,7 +1078,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         nx = unit_of<kDual>(a, w2, rank);
         load_q(nx, steps_of<kDual>(u, 0) > 0, steps_of<kDual>(u, 1) > 0);
       }
-      if (a.split > 1) {
+      if constexpr (kSplit) {
         // Partial rows go where Q and the ring are: both streams end first, and
         // every warp has read Q. (One unit only: all four warps come here.)
         for (int s = 0; s < 2; ++s)
@@ -1047,7 +1093,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncwarp();
-  if (a.split > 1) {
+  if constexpr (kSplit) {
     // ---------------------------------------------------------- joined output
     cluster_sync();
     const Unit u = unit_of<kDual>(a, first_unit, rank);
@@ -1108,13 +1154,11 @@ bool make_map(CUtensorMap* map, const void* base, const AttnArgs& a, int D, int 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool kDual>
-int launch_attention(AttnArgs& a, cudaStream_t stream) {
+template <int D, bool kDual, bool kPath, bool kSplit>
+int launch_kernel(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int sms,
+                  cudaStream_t stream) {
   using P = Plan<D, kDual>;
-  CUtensorMap mk, mv;
-  const int box = a.table ? std::min(a.page_size, kKeys) : kKeys;
-  if (!make_map(&mk, a.k, a, D, box) || !make_map(&mv, a.v, a, D, box))
-    return set_error(SIDBEAM_ERR_CUDA, "beam_attention: tensor map encoding failed");
+  constexpr auto kernel = attention_kernel<D, kDual, kPath, kSplit>;
   static std::mutex mu;
   static bool done[64] = {};
   int dev = 0;
@@ -1123,12 +1167,35 @@ int launch_attention(AttnArgs& a, cudaStream_t stream) {
   {
     std::lock_guard<std::mutex> lock(mu);
     if (dev < 0 || dev >= 64 || !done[dev]) {
-      e = cudaFuncSetAttribute(attention_kernel<D, kDual>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
       if (e != cudaSuccess) return cuda_error(e, "beam_attention: cudaFuncSetAttribute");
       if (dev >= 0 && dev < 64) done[dev] = true;
     }
   }
+  cudaLaunchConfig_t lc{};
+  lc.gridDim = dim3(static_cast<unsigned>(kSplit ? a.units * a.split : std::min(a.units, sms)));
+  lc.blockDim = dim3(kThreads);
+  lc.dynamicSmemBytes = P::kSmem;
+  lc.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = a.split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = kSplit ? 1 : 0;
+  e = cudaLaunchKernelEx(&lc, kernel, mk, mv, a);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return e == cudaSuccess ? SIDBEAM_OK : cuda_error(e, "beam_attention: launch");
+}
+
+template <int D, bool kDual>
+int launch_attention(AttnArgs& a, cudaStream_t stream) {
+  using P = Plan<D, kDual>;
+  CUtensorMap mk, mv;
+  const int box = a.table ? std::min(a.page_size, kKeys) : kKeys;
+  if (!make_map(&mk, a.k, a, D, box) || !make_map(&mv, a.v, a, D, box))
+    return set_error(SIDBEAM_ERR_CUDA, "beam_attention: tensor map encoding failed");
   const int sms = device_sm_count();
   const int unit_rows = P::kTiles * kRows;
   a.pairs = (a.B * a.G + unit_rows - 1) / unit_rows;
@@ -1144,21 +1211,11 @@ int launch_attention(AttnArgs& a, cudaStream_t stream) {
          (4 << a.split_log2) <= max_tiles)
     ++a.split_log2;
   a.split = 1 << a.split_log2;
-  cudaLaunchConfig_t lc{};
-  lc.gridDim = dim3(static_cast<unsigned>(a.split > 1 ? a.units * a.split : std::min(a.units, sms)));
-  lc.blockDim = dim3(kThreads);
-  lc.dynamicSmemBytes = P::kSmem;
-  lc.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = a.split;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  lc.attrs = attr;
-  lc.numAttrs = a.split > 1 ? 1 : 0;
-  e = cudaLaunchKernelEx(&lc, attention_kernel<D, kDual>, mk, mv, a);
-  if (e == cudaSuccess) e = cudaGetLastError();
-  return e == cudaSuccess ? SIDBEAM_OK : cuda_error(e, "beam_attention: launch");
+  if (a.level > 0)
+    return a.split > 1 ? launch_kernel<D, kDual, true, true>(a, mk, mv, sms, stream)
+                       : launch_kernel<D, kDual, true, false>(a, mk, mv, sms, stream);
+  return a.split > 1 ? launch_kernel<D, kDual, false, true>(a, mk, mv, sms, stream)
+                     : launch_kernel<D, kDual, false, false>(a, mk, mv, sms, stream);
 }
 
 bool misaligned(const void* p, uintptr_t to) {
