@@ -71,24 +71,25 @@ constexpr float kNegInf = -INFINITY;
 // through distributed shared memory in rank order.
 constexpr int kRows = 128;
 constexpr int kKeys = 128;
-constexpr int kThreads = 512;  // softmax 0, softmax 1, rows, (MMA, TMA, tails, -)
 constexpr int kMaxSplitLog2 = 3;
 
 template <int D, bool kDual>
 struct Plan {
+  // Warp groups: softmax 0, softmax 1, rows of tile 0, (MMA, TMA, tails, -), and
+  // with two tiles the rows of tile 1.
+  static constexpr int kThreads = kDual ? 640 : 512;
   static constexpr int kTiles = kDual ? 2 : 1;             // row tiles of a unit
   static constexpr int kTile = kKeys * D * 2;              // bytes of a K, V or Q tile
   static constexpr int kHalf = kKeys * 128;                // bytes of 64 of its columns
   static constexpr int kSlots = D == 128 ? (kDual ? 4 : 5) : 8;  // ring of K and V tiles
   static constexpr int kAhead = kDual ? 1 : 2;             // K tiles loaded before a V tile
   static constexpr int kLevels = kDual ? 8 : SIDBEAM_MAX_DEPTH;
-  static constexpr int kStage = kRows * 64;                // 32 columns of a tile's rows, bf16
   static constexpr int kScores = kTiles * kRows * kLevels * 4;
   static constexpr int kSlotTab = kTiles * kRows * kLevels * 2;
   static constexpr int kMl = 2 * kRows * 8;
   static constexpr int kRing = kTiles * kTile;             // offset of the ring (Q is first)
   static constexpr int kAfter = kRing + kSlots * kTile;
-  static constexpr int kSmem = kAfter + kStage + kScores + kSlotTab + kMl + 1024;
+  static constexpr int kSmem = kAfter + kScores + kSlotTab + kMl + 1024;
   static constexpr int kPart = D + 4;                      // floats of a partial row: o, m, l
   static_assert(kTiles * kRows * kPart * 4 <= kAfter, "partial rows fit Q and the ring");
 };
@@ -201,7 +202,7 @@ __device__ __forceinline__ int pos_v(int t, int ahead) { return 2 * t + ahead; }
 // the instance, since every part that a kernel does not have is room in the
 // instruction cache: 128 KB of code measured 15-20% slower than 96 KB.)
 template <int D, bool kDual, bool kPath, bool kSplit>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kDual ? 640 : 512, 1)
     attention_kernel(const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v,
                      const __grid_constant__ AttnArgs a) {
@@ -210,8 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* ring = smem + P::kRing;
-  uint8_t* stage = smem + P::kAfter;
-  float* scores = reinterpret_cast<float*>(stage + P::kStage);  // [tiles][128][kLevels]
+  float* scores = reinterpret_cast<float*>(smem + P::kAfter);  // [tiles][128][kLevels]
   uint16_t* slots = reinterpret_cast<uint16_t*>(scores + P::kScores / 4);
   float2* ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(slots) + P::kSlotTab);
   __shared__ Bars bar;
@@ -250,9 +250,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int quarter = warp & 3;
   const uint32_t quad = static_cast<uint32_t>(quarter * 32) << 16;  // a warp's TMEM lanes
 
-  // Registers: 512 threads start with 128 each; 160 + 160 + 136 + 56 = 4 * 128.
-  if (warp >= 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  // Registers: 640 threads start with 96 each: 112 + 112 + 104 + 104 + 48 = 5 * 96;
+  // 512 start with 128 each: 160 + 160 + 136 + 56 = 4 * 128.
+  if (warp >= 12 && warp < 16) {
+    if constexpr (kDual)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 12) {
       // -------------------------------------------------------- MMA issue
       // One thread for both streams, in the order of the loads. (A thread per
@@ -326,12 +330,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int behind = s ? units1 : units;
               const bool last = j + 1 == n, closing = s || !two;
               const int vp = pos_v(base + j, 1), kp = pos_k(base + j + 1, 1);
+              // (Stream 1 finds the loads that stream 0 has waited for.)
               if (!last) {
                 if (j < 0) wait(&bar.q_full[s], behind);
-                wait_load(kp);
+                if (s == 0) wait_load(kp);
               }
               if (j >= 0) {
-                wait_load(vp);
+                if (s == 0) wait_load(vp);
                 if (j == 0 && behind > 0) wait(&bar.o_empty[s], behind - 1);
                 wait(&bar.p_ready[s], s ? count1++ : count0++);
                 if (!ok) break;
@@ -343,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (closing) free_slot(vp);
                 if (!(s ? two_next : more)) continue;
                 wait(&bar.q_full[s], behind + 1);
-                wait_load(kp);
+                if (s == 0) wait_load(kp);
                 if (s) out1 = true; else out0 = true;
               }
               if (!ok) break;
@@ -508,7 +513,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+    if constexpr (kDual)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
     // ---------------------------------------------------------- softmax
     const int s = warp >> 2;
     const uint32_t t_s = tmem + s * kKeys + quad, t_o = tmem + 256 + s * 128 + quad;
@@ -625,25 +633,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++done;
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
+    if constexpr (kDual)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
     // ---------------------------------------------------------- rows
-    // A warp keeps to the 32 rows of its TMEM lanes (of each tile) throughout, so
-    // its pieces of Q, scores and staging need no barrier beyond the warp.
-    uint8_t* my_stage = stage + quarter * 32 * 64;
+    // A warp group per row tile. A warp keeps to the 32 rows of its TMEM lanes
+    // throughout, so its pieces of Q and the tables need no barrier beyond the warp.
+    const int tile = kDual && warp >= 16 ? 1 : 0;
+    const int first_s = tile, end_s = kDual ? tile + 1 : 2;  // the tile's streams
     const int my0 = quarter * 32;  // first of the warp's rows in a tile
-    int done0 = 0, done1 = 0;      // units behind, of each stream
+    int done0 = 0, done1 = 0;      // units behind, of the tile's streams
     bool ok = true;
     // (2^32 / 1 does not fit the magic factor.)
     auto beam_of = [&](int i) {
       return a.G == 1 ? i : static_cast<int>(__umulhi(static_cast<uint32_t>(i), a.g_magic));
     };
     // The warp's valid rows of a tile.
-    auto rows_in = [&](const Unit& u, int tile) {
+    auto rows_in = [&](const Unit& u) {
       return min(32, u.rows - tile * kRows - my0);
     };
     // Elements from the row of the unit's first beam to this lane's row of a tile
     // (strides are below 2^24, a unit has at most 256 beams).
-    auto row_off = [&](const Unit& u, int tile, int64_t row_stride) {
+    auto row_off = [&](const Unit& u, int64_t row_stride) {
       const int i = u.row0 + tile * kRows + my0 + lane, b = beam_of(i);
       return static_cast<uint32_t>(b - beam_of(u.row0)) * static_cast<uint32_t>(row_stride) +
              static_cast<uint32_t>((i - b * a.G) * D);
@@ -658,80 +670,59 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     const uint32_t slot16 = static_cast<uint32_t>(a.Hkv * (D / 8));
 
-    // Q of unit u into its tiles, behind the last product with the ones before.
-    // (`more0`, `more1`: the unit before, not yet counted, used the stream.)
-    auto load_q = [&](const Unit& u, int more0, int more1) {
+    // Q of unit u into the tile, behind the last product with the one before.
+    // (`more`: the unit before, not yet counted, used it.)
+    auto load_q = [&](const Unit& u, int more) {
       constexpr int kUnits = D / 8, kPer = 32 / kUnits;
       const int c = lane % kUnits;
-#pragma unroll 1
-      for (int t = 0; t < P::kTiles; ++t) {
-        const int users = t ? done1 + more1 : done0 + more0;
-        if (users > 0 && !warp_wait(&bar.q_empty[t], users - 1, &bar.abort, a.status)) ok = false;
-        if (!ok) return;
-        uint8_t* qt = smem + t * P::kTile;
-        const int valid = rows_in(u, t);
-        const uint32_t off = row_off(u, t, a.q_stride);
-        const __nv_bfloat16* src = a.q + row_base(u, a.q_stride) + c * 8;
-#pragma unroll 1
-        for (int lr = lane / kUnits; lr < 32; lr += kPer) {
-          const uint32_t at = __shfl_sync(0xFFFFFFFFu, off, lr);
-          if (lr < valid) cp_async16(qt + unit_at(my0 + lr, c), src + at);
-        }
+      const int users = done0 + more;
+      if (users > 0 && !warp_wait(&bar.q_empty[tile], users - 1, &bar.abort, a.status)) ok = false;
+      if (!ok) return;
+      uint8_t* qt = smem + tile * P::kTile;
+      const int valid = rows_in(u);
+      const uint32_t off = row_off(u, a.q_stride);
+      const __nv_bfloat16* src = a.q + row_base(u, a.q_stride) + c * 8;
+#pragma unroll 2
+      for (int lr = lane / kUnits; lr < 32; lr += kPer) {
+        const uint32_t at = __shfl_sync(0xFFFFFFFFu, off, lr);
+        if (lr < valid) cp_async16(qt + unit_at(my0 + lr, c), src + at);
       }
       cp_async_wait();
       __syncwarp();
+      if (a.q_flip) {
 #pragma unroll 1
-      for (int t = 0; t < P::kTiles; ++t) {
-        if (a.q_flip) {
-          uint8_t* qt = smem + t * P::kTile;
-#pragma unroll 1
-          for (int e = lane; e < 32 * kUnits; e += 32) {
-            uint4* q = reinterpret_cast<uint4*>(qt + unit_at(my0 + e / kUnits, e % kUnits));
-            *q = make_uint4(q->x ^ a.q_flip, q->y ^ a.q_flip, q->z ^ a.q_flip, q->w ^ a.q_flip);
-          }
+        for (int e = lane; e < 32 * kUnits; e += 32) {
+          uint4* q = reinterpret_cast<uint4*>(qt + unit_at(my0 + e / kUnits, e % kUnits));
+          *q = make_uint4(q->x ^ a.q_flip, q->y ^ a.q_flip, q->z ^ a.q_flip, q->w ^ a.q_flip);
         }
-        fence_proxy_async();
-        __syncwarp();
-        if (steps_of<kDual>(u, t) > 0 && lane == 0) mbar_arrive(&bar.q_full[t]);
       }
+      fence_proxy_async();
+      __syncwarp();
+      if (steps_of<kDual>(u, tile) > 0 && lane == 0) mbar_arrive(&bar.q_full[tile]);
     };
 
-    // The slots of the rows' ancestors at every level, both tiles' links followed
-    // together; a dead row has none. Returns a bit per tile: this lane's row is dead.
+    // The slots of the rows' ancestors at every level. Returns whether this lane's
+    // row is dead.
     auto walk_path = [&](const Unit& u) {
-      int at[P::kTiles];
-#pragma unroll
-      for (int t = 0; t < P::kTiles; ++t)
-        at[t] = lane < rows_in(u, t) ? beam_of(u.row0 + t * kRows + my0 + lane) : -1;
+      uint16_t* tab = slots + (tile * kRows + my0) * P::kLevels;
+      int at = lane < rows_in(u) ? beam_of(u.row0 + tile * kRows + my0 + lane) : -1;
 #pragma unroll 1
       for (int v = a.level - 1; v >= 0; --v) {
-        const int32_t* bp = a.bp + (static_cast<int64_t>(v) * a.R + u.r) * a.B;
-        int p[P::kTiles];
-#pragma unroll
-        for (int t = 0; t < P::kTiles; ++t) {
-          slots[(t * kRows + my0 + lane) * P::kLevels + v] = static_cast<uint16_t>(at[t]);
-          p[t] = at[t] < 0 ? -1 : bp[at[t]];
-        }
-#pragma unroll
-        for (int t = 0; t < P::kTiles; ++t) at[t] = p[t] < 0 || (v > 0 && p[t] >= a.B) ? -1 : p[t];
+        tab[lane * P::kLevels + v] = static_cast<uint16_t>(at);
+        const int p = at < 0 ? -1 : a.bp[(static_cast<int64_t>(v) * a.R + u.r) * a.B + at];
+        at = p < 0 || (v > 0 && p >= a.B) ? -1 : p;
       }
       __syncwarp();
       // Dead rows (and those past the last) take a live row's slots, so that what
       // is loaded for them is a live beam's; their weights are zero.
-      uint32_t dead = 0u;
-#pragma unroll
-      for (int t = 0; t < P::kTiles; ++t) {
-        const uint32_t live = __ballot_sync(0xFFFFFFFFu, at[t] >= 0);
-        if (at[t] < 0) {
-          dead |= 1u << t;
-          uint16_t* tab = slots + (t * kRows + my0) * P::kLevels;
+      const uint32_t live = __ballot_sync(0xFFFFFFFFu, at >= 0);
+      if (at < 0) {
 #pragma unroll 1
-          for (int v = 0; v < a.level; ++v)
-            tab[lane * P::kLevels + v] = live ? tab[(__ffs(live) - 1) * P::kLevels + v] : 0;
-        }
+        for (int v = 0; v < a.level; ++v)
+          tab[lane * P::kLevels + v] = live ? tab[(__ffs(live) - 1) * P::kLevels + v] : 0;
       }
       __syncwarp();
-      return dead;
+      return at < 0;
     };
 
     // The rows' own softmax over their ancestors, for the warp's rows of a tile,
@@ -742,8 +733,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the time: a lane's loads then touch 32 lines at once.) The weighted values,
     // against the path's maximum, wait in the rows' places of the output (bf16);
     // maximum and sum stay in the row's first two table entries.
-    auto attend_path = [&](const Unit& u, int tile, bool dead) {
-      const int valid = rows_in(u, tile);
+    auto attend_path = [&](const Unit& u, bool dead) {
+      const int valid = rows_in(u);
       if (valid <= 0) return;
       const uint16_t* tab = slots + (tile * kRows + my0) * P::kLevels;
       float* xs = scores + (tile * kRows + my0) * P::kLevels;
@@ -753,52 +744,66 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint4* kb16 = reinterpret_cast<const uint4*>(a.kb);
       const uint4* vb16 = reinterpret_cast<const uint4*>(a.vb);
       const uint32_t base16 = beam_base(u);
-      // ---- scores
-#pragma unroll 1
-      for (int rg = 0; rg < valid; rg += 16) {
+      // ---- scores: rounds of 16 rows x 8 beams x 2 levels, a round's loads in
+      // flight under the round before
+      {
         constexpr int kWords = D / 32;  // 16-byte words of a lane's quarter of D
-        const int b0 = beam_of(i0 + rg), b_end = beam_of(i0 + min(rg + 15, valid - 1));
-        const int j_lo = beam_of(i0 + rg + n8) - b0, j_hi = beam_of(i0 + rg + n8 + 8) - b0;
-#pragma unroll 1
-        for (int n0 = 0; n0 <= b_end - b0; n0 += 8) {
-          // This lane's key: beam b0 + n0 + n8 (or the last one, again), through
-          // its first row in the group.
+        const int rounds_v = (a.level + 1) >> 1;
+        uint4 kw[2][kWords];
+        // This lane's key: beam b0 + n0 + n8 (or the last one, again), through its
+        // first row in the group.
+        auto load = [&](int rg, int n0, int v0) {
+          const int b0 = beam_of(i0 + rg), b_end = beam_of(i0 + min(rg + 15, valid - 1));
           const uint16_t* of =
               tab + max(rg, min(b0 + n0 + n8, b_end) * a.G - i0) * P::kLevels;
-          const int lo = j_lo - n0, hi = j_hi - n0;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int v = min(v0 + e, a.level - 1);
+            const uint4* src =
+                kb16 + (base16 + v * a.level16 + of[v] * slot16 + c * static_cast<uint32_t>(kWords));
+#pragma unroll
+            for (int k = 0; k < kWords; ++k) kw[e][k] = src[k];
+          }
+        };
+        load(0, 0, 0);
+        int rg = 0, n0 = 0, v0 = 0;
 #pragma unroll 1
-          for (int v0 = 0; v0 < a.level; v0 += 2) {  // two levels' loads in flight
-            uint4 kw[2][kWords];
+        while (rg < valid) {
+          const int b0 = beam_of(i0 + rg), b_end = beam_of(i0 + min(rg + 15, valid - 1));
+          const int lo = beam_of(i0 + rg + n8) - b0 - n0, hi = beam_of(i0 + rg + n8 + 8) - b0 - n0;
+          float z[2][4] = {};
+#pragma unroll
+          for (int k = 0; k < kWords; ++k) {
+            const uint4 qa =
+                *reinterpret_cast<const uint4*>(qt + unit_at(my0 + rg + n8, c * kWords + k));
+            const uint4 qb =
+                *reinterpret_cast<const uint4*>(qt + unit_at(my0 + rg + n8 + 8, c * kWords + k));
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int v = min(v0 + e, a.level - 1);
-              const uint4* src =
-                  kb16 + (base16 + v * a.level16 + of[v] * slot16 + c * static_cast<uint32_t>(kWords));
-#pragma unroll
-              for (int k = 0; k < kWords; ++k) kw[e][k] = src[k];
+              mma_16816(z[e], qa.x, qb.x, qa.y, qb.y, kw[e][k].x, kw[e][k].y);
+              mma_16816(z[e], qa.z, qb.z, qa.w, qb.w, kw[e][k].z, kw[e][k].w);
             }
-            float z[2][4] = {};
-#pragma unroll
-            for (int k = 0; k < kWords; ++k) {
-              const uint4 qa =
-                  *reinterpret_cast<const uint4*>(qt + unit_at(my0 + rg + n8, c * kWords + k));
-              const uint4 qb =
-                  *reinterpret_cast<const uint4*>(qt + unit_at(my0 + rg + n8 + 8, c * kWords + k));
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                mma_16816(z[e], qa.x, qb.x, qa.y, qb.y, kw[e][k].x, kw[e][k].y);
-                mma_16816(z[e], qa.z, qb.z, qa.w, qb.w, kw[e][k].z, kw[e][k].w);
-              }
+          }
+          const int rg_now = rg, v_now = v0;
+          v0 += 2;
+          if (v0 >= 2 * rounds_v) {
+            v0 = 0;
+            n0 += 8;
+            if (n0 > b_end - b0) {
+              n0 = 0;
+              rg += 16;
             }
+          }
+          if (rg < valid) load(rg, n0, v0);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              if (v0 + e < a.level) {
-                if ((lo >> 1) == c)
-                  xs[(rg + n8) * P::kLevels + v0 + e] = (lo & 1 ? z[e][1] : z[e][0]) * a.scale_log2;
-                if ((hi >> 1) == c)
-                  xs[(rg + n8 + 8) * P::kLevels + v0 + e] =
-                      (hi & 1 ? z[e][3] : z[e][2]) * a.scale_log2;
-              }
+          for (int e = 0; e < 2; ++e) {
+            if (v_now + e < a.level) {
+              if ((lo >> 1) == c)
+                xs[(rg_now + n8) * P::kLevels + v_now + e] =
+                    (lo & 1 ? z[e][1] : z[e][0]) * a.scale_log2;
+              if ((hi >> 1) == c)
+                xs[(rg_now + n8 + 8) * P::kLevels + v_now + e] =
+                    (hi & 1 ? z[e][3] : z[e][2]) * a.scale_log2;
             }
           }
         }
@@ -817,63 +822,85 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-      // ---- values, 16 rows by 64 columns at a time
-      const uint32_t off = row_off(u, tile, a.out_stride);
+      // ---- values: parts of 16 rows by 64 columns, in rounds of 8 beams x 2 levels,
+      // a round's loads in flight under the round before
+      const uint32_t off = row_off(u, a.out_stride);
       __nv_bfloat16* out = a.out + row_base(u, a.out_stride);
-#pragma unroll 1
-      for (int part = 0; part < 2 * (D / 64); ++part) {
-        const int rg = part / (D / 64) * 16, d0 = part % (D / 64) * 64;
-        if (rg >= valid) break;
-        float y[8][4] = {};
+      uint4 vw[4];
+      // Keys of this lane: beams b0 + n0 + 2c, + 1 (or the last one, again) at two
+      // levels; columns d0 + 8 n8 .. + 7 of each.
+      auto load = [&](int rg, int d0, int n0, int v0) {
         const int b0 = beam_of(i0 + rg), b_end = beam_of(i0 + min(rg + 15, valid - 1));
-        const int j_lo = beam_of(i0 + rg + n8) - b0, j_hi = beam_of(i0 + rg + n8 + 8) - b0;
+        const int kb = b0 + n0 + 2 * c;
+        const uint16_t* of0 = tab + max(rg, min(kb, b_end) * a.G - i0) * P::kLevels;
+        const uint16_t* of1 = tab + max(rg, min(kb + 1, b_end) * a.G - i0) * P::kLevels;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int v = min(v0 + (e >> 1), a.level - 1);
+          vw[e] = vb16[base16 + v * a.level16 + (e & 1 ? of1 : of0)[v] * slot16 +
+                       static_cast<uint32_t>(d0 / 8 + n8)];
+        }
+      };
+      load(0, 0, 0, 0);
+      float y[8][4];
+      int rg = 0, d0 = 0, n0 = 0, v0 = 0;
 #pragma unroll 1
-        for (int n0 = 0; n0 <= b_end - b0; n0 += 8) {
-          // Keys of this lane: beams b0 + n0 + 2c, + 1 at two levels; columns
-          // d0 + 8 n8 .. + 7 of each.
-          const int kb = b0 + n0 + 2 * c, lo = j_lo - n0, hi = j_hi - n0;
-          const uint16_t* of0 = tab + max(rg, min(kb, b_end) * a.G - i0) * P::kLevels;
-          const uint16_t* of1 = tab + max(rg, min(kb + 1, b_end) * a.G - i0) * P::kLevels;
-#pragma unroll 1
-          for (int v0 = 0; v0 < a.level; v0 += 2) {
-            uint4 vw[4];
+      while (rg < valid) {
+        const int b0 = beam_of(i0 + rg), b_end = beam_of(i0 + min(rg + 15, valid - 1));
+        const int lo = beam_of(i0 + rg + n8) - b0 - n0, hi = beam_of(i0 + rg + n8 + 8) - b0 - n0;
+        if (n0 == 0 && v0 == 0) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int v = min(v0 + (e >> 1), a.level - 1);
-              vw[e] = vb16[base16 + v * a.level16 + (e & 1 ? of1 : of0)[v] * slot16 +
-                           static_cast<uint32_t>(d0 / 8 + n8)];
-            }
-            // Weights: a row's in the place of its own beam, as the sum of two bf16
-            // (its values are rounded once on their way through the output, which
-            // takes what rounding the weights is allowed).
-            uint32_t aw[4], ar[4];
+          for (int k = 0; k < 8; ++k)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int at = e & 1 ? hi : lo, v = v0 + (e >> 1);
-              const float wt = (at >> 1) == c && v < a.level
-                                   ? xs[(rg + n8 + (e & 1) * 8) * P::kLevels + v]
-                                   : 0.f;
-              const float head = __uint_as_float(__float_as_uint(wt) & 0xFFFF0000u);
-              aw[e] = at & 1 ? bf16x2(0.f, head) : bf16x2(head, 0.f);
-              ar[e] = at & 1 ? bf16x2(0.f, wt - head) : bf16x2(wt - head, 0.f);
-            }
-            const uint32_t w[4][4] = {{vw[0].x, vw[0].y, vw[0].z, vw[0].w},
-                                      {vw[1].x, vw[1].y, vw[1].z, vw[1].w},
-                                      {vw[2].x, vw[2].y, vw[2].z, vw[2].w},
-                                      {vw[3].x, vw[3].y, vw[3].z, vw[3].w}};
+            for (int e = 0; e < 4; ++e) y[k][e] = 0.f;
+        }
+        // Weights: a row's in the place of its own beam, as the sum of two bf16
+        // (its values are rounded once on their way through the output, which
+        // takes what rounding the weights is allowed).
+        uint32_t aw[4], ar[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t e0 = __byte_perm(w[0][k], w[1][k], 0x5410);
-              const uint32_t e1 = __byte_perm(w[2][k], w[3][k], 0x5410);
-              const uint32_t o0 = __byte_perm(w[0][k], w[1][k], 0x7632);
-              const uint32_t o1 = __byte_perm(w[2][k], w[3][k], 0x7632);
-              mma_16816(y[2 * k], aw[0], aw[1], aw[2], aw[3], e0, e1);
-              mma_16816(y[2 * k + 1], aw[0], aw[1], aw[2], aw[3], o0, o1);
-              mma_16816(y[2 * k], ar[0], ar[1], ar[2], ar[3], e0, e1);
-              mma_16816(y[2 * k + 1], ar[0], ar[1], ar[2], ar[3], o0, o1);
+        for (int e = 0; e < 4; ++e) {
+          const int at = e & 1 ? hi : lo, v = v0 + (e >> 1);
+          const float wt = (at >> 1) == c && v < a.level
+                               ? xs[(rg + n8 + (e & 1) * 8) * P::kLevels + v]
+                               : 0.f;
+          const float head = __uint_as_float(__float_as_uint(wt) & 0xFFFF0000u);
+          aw[e] = at & 1 ? bf16x2(0.f, head) : bf16x2(head, 0.f);
+          ar[e] = at & 1 ? bf16x2(0.f, wt - head) : bf16x2(wt - head, 0.f);
+        }
+        const uint32_t w[4][4] = {{vw[0].x, vw[0].y, vw[0].z, vw[0].w},
+                                  {vw[1].x, vw[1].y, vw[1].z, vw[1].w},
+                                  {vw[2].x, vw[2].y, vw[2].z, vw[2].w},
+                                  {vw[3].x, vw[3].y, vw[3].z, vw[3].w}};
+        const int rg_now = rg, d_now = d0;
+        v0 += 2;
+        bool part_done = false;
+        if (v0 >= a.level) {
+          v0 = 0;
+          n0 += 8;
+          if (n0 > b_end - b0) {
+            n0 = 0;
+            part_done = true;
+            d0 += 64;
+            if (d0 == D) {
+              d0 = 0;
+              rg += 16;
             }
           }
         }
+        if (rg < valid) load(rg, d0, n0, v0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t e0 = __byte_perm(w[0][k], w[1][k], 0x5410);
+          const uint32_t e1 = __byte_perm(w[2][k], w[3][k], 0x5410);
+          const uint32_t o0 = __byte_perm(w[0][k], w[1][k], 0x7632);
+          const uint32_t o1 = __byte_perm(w[2][k], w[3][k], 0x7632);
+          mma_16816(y[2 * k], aw[0], aw[1], aw[2], aw[3], e0, e1);
+          mma_16816(y[2 * k + 1], aw[0], aw[1], aw[2], aw[3], o0, o1);
+          mma_16816(y[2 * k], ar[0], ar[1], ar[2], ar[3], e0, e1);
+          mma_16816(y[2 * k + 1], ar[0], ar[1], ar[2], ar[3], o0, o1);
+        }
+        if (!part_done) continue;
         // An infinity or NaN in one beam's values would reach its neighbours
         // through their zero weights: such a part is added up row by row.
         float all = 0.f;
@@ -881,10 +908,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < 8; ++k) all += (y[k][0] + y[k][1]) + (y[k][2] + y[k][3]);
         if (__any_sync(0xFFFFFFFFu, !(fabsf(all) < 3.0e38f))) {
 #pragma unroll 1
-          for (int lr = rg; lr < min(rg + 16, valid); ++lr) {
+          for (int lr = rg_now; lr < min(rg_now + 16, valid); ++lr) {
             const uint32_t at = __shfl_sync(0xFFFFFFFFu, off, lr);
 #pragma unroll 1
-            for (int d = d0 + lane; d < d0 + 64; d += 32) {
+            for (int d = d_now + lane; d < d_now + 64; d += 32) {
               float z = 0.f;
 #pragma unroll 1
               for (int v = 0; v < a.level; ++v) {
@@ -896,13 +923,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         } else {
-          // This lane: columns d0 + 16 c .. + 15 of rows rg + n8 and + 8.
+          // This lane: columns 16 c .. + 15 of the part's rows n8 and + 8.
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            const int lr = rg + n8 + half * 8, e = half * 2;
+            const int lr = rg_now + n8 + half * 8, e = half * 2;
             const uint32_t at = __shfl_sync(0xFFFFFFFFu, off, lr);
             if (lr < valid) {
-              uint4* dst = reinterpret_cast<uint4*>(out + at + d0 + c * 16);
+              uint4* dst = reinterpret_cast<uint4*>(out + at + d_now + c * 16);
               dst[0] = make_uint4(bf16x2(y[0][e], y[1][e]), bf16x2(y[2][e], y[3][e]),
                                   bf16x2(y[4][e], y[5][e]), bf16x2(y[6][e], y[7][e]));
               dst[1] = make_uint4(bf16x2(y[0][e + 1], y[1][e + 1]), bf16x2(y[2][e + 1], y[3][e + 1]),
@@ -918,11 +945,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // Joins the streams and the path of the warp's rows of a tile, a row per lane,
     // and writes them: bf16 rows, or (split keys) partial rows in fp32.
-    auto finish = [&](const Unit& u, int tile, bool dead) {
-      const int valid = rows_in(u, tile);
-      const int s_end = kDual ? tile + 1 : 2;
+    auto finish = [&](const Unit& u, bool dead) {
+      const int valid = rows_in(u);
       const bool path = kPath && rank == 0;
-      const uint32_t off = row_off(u, tile, a.out_stride);
+      const uint32_t off = row_off(u, a.out_stride);
       __nv_bfloat16* out = a.out + row_base(u, a.out_stride);
       float mp = kNegInf, lp = 0.f;
       if (path && lane < valid) {
@@ -934,9 +960,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float2 st_a = make_float2(kNegInf, 0.f), st_b = st_a;
 #pragma unroll 1
-      for (int s = kDual ? tile : 0; s < s_end; ++s) {
+      for (int s = first_s; s < end_s; ++s) {
         if (steps_of<kDual>(u, s) == 0) continue;
-        const int done = s ? done1 : done0;
+        const int done = !kDual && s ? done1 : done0;
         if (!warp_wait(&bar.ml_full[s], done, &bar.abort, a.status) ||
             !warp_wait(&bar.o_full[s], done, &bar.abort, a.status)) {
           ok = false;
@@ -973,7 +999,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool read_a = valid > 0 && steps_of<kDual>(u, sa) > 0;
       const bool read_b = !kDual && valid > 0 && steps_of<kDual>(u, 1) > 0;
       const bool with_path = kPath && fp > 0.f && lane < valid;
-      const int u4 = lane & 3;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint4 pw[4];
@@ -1001,10 +1026,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();
           __syncwarp();
 #pragma unroll 1
-          for (int s = kDual ? tile : 0; s < s_end; ++s)
+          for (int s = first_s; s < end_s; ++s)
             if (steps_of<kDual>(u, s) > 0) {
               if (lane == 0) mbar_arrive(&bar.o_empty[s]);
-              if (s) ++done1; else ++done0;
+              if (!kDual && s) ++done1; else ++done0;
             }
         }
         if (with_path) {
@@ -1028,22 +1053,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                   make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           }
         } else {
-        // From a row per lane to 64-byte pieces of rows.
+        if (lane < valid) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          *reinterpret_cast<uint4*>(my_stage + lane * 64 + ((k ^ (lane >> 1)) & 3) * 16) =
-              make_uint4(bf16x2(o[k * 8], o[k * 8 + 1]), bf16x2(o[k * 8 + 2], o[k * 8 + 3]),
-                         bf16x2(o[k * 8 + 4], o[k * 8 + 5]), bf16x2(o[k * 8 + 6], o[k * 8 + 7]));
-        __syncwarp();
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int lr = q * 8 + (lane >> 2);
-          const uint32_t at = __shfl_sync(0xFFFFFFFFu, off, lr);
-          const uint4 w = *reinterpret_cast<const uint4*>(my_stage + lr * 64 +
-                                                          ((u4 ^ (lr >> 1)) & 3) * 16);
-          if (lr < valid) *reinterpret_cast<uint4*>(out + at + c + u4 * 8) = w;
+          for (int e = 0; e < 32; e += 8)
+            *reinterpret_cast<uint4*>(out + off + c + e) =
+                make_uint4(bf16x2(o[e], o[e + 1]), bf16x2(o[e + 2], o[e + 3]),
+                           bf16x2(o[e + 4], o[e + 5]), bf16x2(o[e + 6], o[e + 7]));
         }
-        __syncwarp();
         }
       }
     };
@@ -1051,44 +1067,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     Unit u;
     if (first_unit < a.units) {
       u = unit_of<kDual>(a, first_unit, rank);
-      load_q(u, 0, 0);
+      load_q(u, 0);
     }
     for (int w = first_unit; ok && w < a.units; w += stride) {
-      uint32_t dead = 0u;  // bit t: this lane's row of tile t
-      if (w + stride < a.units) {
+      const bool have_next = w + stride < a.units;
+      Unit nx = u;
+      if (have_next) {
         // The next unit's q on its way to L2.
-        const Unit nx = unit_of<kDual>(a, w + stride, rank);
-#pragma unroll 1
-        for (int t = 0; t < P::kTiles; ++t)
-          if (lane < rows_in(nx, t))
-            for (int c = 0; c < D; c += 64)
-              asm volatile("prefetch.global.L2 [%0];" ::"l"(a.q + row_base(nx, a.q_stride) +
-                                                            row_off(nx, t, a.q_stride) + c));
+        nx = unit_of<kDual>(a, w + stride, rank);
+        if (lane < rows_in(nx))
+          for (int c = 0; c < D; c += 64)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(a.q + row_base(nx, a.q_stride) +
+                                                          row_off(nx, a.q_stride) + c));
       }
+      bool dead = false;
       if constexpr (kPath) {
         dead = walk_path(u);
-#pragma unroll 1
-        for (int t = 0; rank == 0 && t * kRows < u.rows; ++t)
-          attend_path(u, t, (dead >> t & 1u) != 0u);
+        if (rank == 0) attend_path(u, dead);
       }
       // The next unit's Q comes in once this one's last products are done.
-      const int w2 = w + stride;
-      Unit nx = u;
-      if (w2 < a.units) {
-        nx = unit_of<kDual>(a, w2, rank);
-        load_q(nx, steps_of<kDual>(u, 0) > 0, steps_of<kDual>(u, 1) > 0);
-      }
+      if (have_next) load_q(nx, steps_of<kDual>(u, tile) > 0);
       if constexpr (kSplit) {
         // Partial rows go where Q and the ring are: both streams end first, and
-        // every warp has read Q. (One unit only: all four warps come here.)
+        // every warp has read Q. (One unit only: all of these warps come here.)
         for (int s = 0; s < 2; ++s)
-          if (steps_of<kDual>(u, s) > 0 &&
-              !warp_wait(&bar.o_full[s], s ? done1 : done0, &bar.abort, a.status))
+          if (steps_of<kDual>(u, s) > 0 && !warp_wait(&bar.o_full[s], 0, &bar.abort, a.status))
             ok = false;
-        named_sync(1, 128);
+        named_sync(1, kDual ? 256 : 128);
       }
-#pragma unroll 1
-      for (int t = 0; ok && t * kRows < u.rows; ++t) finish(u, t, (dead >> t & 1u) != 0u);
+      if (ok) finish(u, dead);
       u = nx;
     }
   }
@@ -1098,7 +1105,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync();
     const Unit u = unit_of<kDual>(a, first_unit, rank);
     const float* part = reinterpret_cast<const float*>(smem);
-    for (int i = rank * (kThreads / 32) + warp; i < u.rows; i += (kThreads / 32) * a.split) {
+    constexpr int kWarps = P::kThreads / 32;
+    for (int i = rank * kWarps + warp; i < u.rows; i += kWarps * a.split) {
       const float* mine = part + i * P::kPart;
       float mp = kNegInf, lp = 0.f;
       if (lane < a.split) {
@@ -1174,7 +1182,7 @@ int launch_kernel(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& m
   }
   cudaLaunchConfig_t lc{};
   lc.gridDim = dim3(static_cast<unsigned>(kSplit ? a.units * a.split : std::min(a.units, sms)));
-  lc.blockDim = dim3(kThreads);
+  lc.blockDim = dim3(P::kThreads);
   lc.dynamicSmemBytes = P::kSmem;
   lc.stream = stream;
   cudaLaunchAttribute attr[1];

@@ -36,6 +36,7 @@ constexpr int kWaitLooks = 1 << 22;
 // One thread:
 __device__ __forceinline__ bool lane_wait(uint64_t* bar, uint32_t phase, volatile int* abort,
                                           uint32_t* status) {
+  if (mbar_try_wait(bar, phase & 1u)) return true;  // (the loop alone: 2.4x the cycles)
   int looks = 0;
 #pragma unroll 1
   while (!mbar_try_wait(bar, phase & 1u)) {
