@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kDual ? 640 : 512, 1)
   const int quarter = warp & 3;
   const uint32_t quad = static_cast<uint32_t>(quarter * 32) << 16;  // a warp's TMEM lanes
 
-  // Registers: 640 threads start with 96 each: 112 + 112 + 104 + 104 + 48 = 5 * 96;
+  // Registers: 640 threads start with 96 each: 96 + 96 + 120 + 120 + 48 = 5 * 96;
   // 512 start with 128 each: 160 + 160 + 136 + 56 = 4 * 128.
   if (warp >= 12 && warp < 16) {
     if constexpr (kDual)
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(kDual ? 640 : 512, 1)
     }
   } else if (warp < 8) {
     if constexpr (kDual)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
     else
       asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
     // ---------------------------------------------------------- softmax
@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(kDual ? 640 : 512, 1)
     }
   } else {
     if constexpr (kDual)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
     else
       asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
     // ---------------------------------------------------------- rows
@@ -744,26 +744,21 @@ __global__ void __launch_bounds__(kDual ? 640 : 512, 1)
       const uint4* kb16 = reinterpret_cast<const uint4*>(a.kb);
       const uint4* vb16 = reinterpret_cast<const uint4*>(a.vb);
       const uint32_t base16 = beam_base(u);
-      // ---- scores: rounds of 16 rows x 8 beams x 2 levels, a round's loads in
+      // ---- scores: rounds of 16 rows x 8 beams x a level, a round's loads in
       // flight under the round before
       {
         constexpr int kWords = D / 32;  // 16-byte words of a lane's quarter of D
-        const int rounds_v = (a.level + 1) >> 1;
-        uint4 kw[2][kWords];
+        uint4 kw[kWords];
         // This lane's key: beam b0 + n0 + n8 (or the last one, again), through its
         // first row in the group.
         auto load = [&](int rg, int n0, int v0) {
           const int b0 = beam_of(i0 + rg), b_end = beam_of(i0 + min(rg + 15, valid - 1));
           const uint16_t* of =
               tab + max(rg, min(b0 + n0 + n8, b_end) * a.G - i0) * P::kLevels;
+          const uint4* src =
+              kb16 + (base16 + v0 * a.level16 + of[v0] * slot16 + c * static_cast<uint32_t>(kWords));
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int v = min(v0 + e, a.level - 1);
-            const uint4* src =
-                kb16 + (base16 + v * a.level16 + of[v] * slot16 + c * static_cast<uint32_t>(kWords));
-#pragma unroll
-            for (int k = 0; k < kWords; ++k) kw[e][k] = src[k];
-          }
+          for (int k = 0; k < kWords; ++k) kw[k] = src[k];
         };
         load(0, 0, 0);
         int rg = 0, n0 = 0, v0 = 0;
@@ -771,22 +766,18 @@ __global__ void __launch_bounds__(kDual ? 640 : 512, 1)
         while (rg < valid) {
           const int b0 = beam_of(i0 + rg), b_end = beam_of(i0 + min(rg + 15, valid - 1));
           const int lo = beam_of(i0 + rg + n8) - b0 - n0, hi = beam_of(i0 + rg + n8 + 8) - b0 - n0;
-          float z[2][4] = {};
+          float z[2][4] = {};  // two chains, added below
 #pragma unroll
           for (int k = 0; k < kWords; ++k) {
             const uint4 qa =
                 *reinterpret_cast<const uint4*>(qt + unit_at(my0 + rg + n8, c * kWords + k));
             const uint4 qb =
                 *reinterpret_cast<const uint4*>(qt + unit_at(my0 + rg + n8 + 8, c * kWords + k));
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              mma_16816(z[e], qa.x, qb.x, qa.y, qb.y, kw[e][k].x, kw[e][k].y);
-              mma_16816(z[e], qa.z, qb.z, qa.w, qb.w, kw[e][k].z, kw[e][k].w);
-            }
+            mma_16816(z[0], qa.x, qb.x, qa.y, qb.y, kw[k].x, kw[k].y);
+            mma_16816(z[1], qa.z, qb.z, qa.w, qb.w, kw[k].z, kw[k].w);
           }
           const int rg_now = rg, v_now = v0;
-          v0 += 2;
-          if (v0 >= 2 * rounds_v) {
+          if (++v0 == a.level) {
             v0 = 0;
             n0 += 8;
             if (n0 > b_end - b0) {
@@ -795,17 +786,12 @@ __global__ void __launch_bounds__(kDual ? 640 : 512, 1)
             }
           }
           if (rg < valid) load(rg, n0, v0);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            if (v_now + e < a.level) {
-              if ((lo >> 1) == c)
-                xs[(rg_now + n8) * P::kLevels + v_now + e] =
-                    (lo & 1 ? z[e][1] : z[e][0]) * a.scale_log2;
-              if ((hi >> 1) == c)
-                xs[(rg_now + n8 + 8) * P::kLevels + v_now + e] =
-                    (hi & 1 ? z[e][3] : z[e][2]) * a.scale_log2;
-            }
-          }
+          if ((lo >> 1) == c)
+            xs[(rg_now + n8) * P::kLevels + v_now] =
+                (lo & 1 ? z[0][1] + z[1][1] : z[0][0] + z[1][0]) * a.scale_log2;
+          if ((hi >> 1) == c)
+            xs[(rg_now + n8 + 8) * P::kLevels + v_now] =
+                (hi & 1 ? z[0][3] + z[1][3] : z[0][2] + z[1][2]) * a.scale_log2;
         }
       }
       __syncwarp();
@@ -822,13 +808,13 @@ __global__ void __launch_bounds__(kDual ? 640 : 512, 1)
         }
       }
       __syncwarp();
-      // ---- values: parts of 16 rows by 64 columns, in rounds of 8 beams x 2 levels,
+      // ---- values: parts of 16 rows by 32 columns, in rounds of 8 beams x 2 levels,
       // a round's loads in flight under the round before
       const uint32_t off = row_off(u, a.out_stride);
       __nv_bfloat16* out = a.out + row_base(u, a.out_stride);
-      uint4 vw[4];
+      uint2 vw[4];
       // Keys of this lane: beams b0 + n0 + 2c, + 1 (or the last one, again) at two
-      // levels; columns d0 + 8 n8 .. + 7 of each.
+      // levels; columns d0 + 4 n8 .. + 3 of each.
       auto load = [&](int rg, int d0, int n0, int v0) {
         const int b0 = beam_of(i0 + rg), b_end = beam_of(i0 + min(rg + 15, valid - 1));
         const int kb = b0 + n0 + 2 * c;
@@ -837,12 +823,12 @@ __global__ void __launch_bounds__(kDual ? 640 : 512, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int v = min(v0 + (e >> 1), a.level - 1);
-          vw[e] = vb16[base16 + v * a.level16 + (e & 1 ? of1 : of0)[v] * slot16 +
-                       static_cast<uint32_t>(d0 / 8 + n8)];
+          vw[e] = reinterpret_cast<const uint2*>(
+              vb16 + (base16 + v * a.level16 + (e & 1 ? of1 : of0)[v] * slot16))[d0 / 4 + n8];
         }
       };
       load(0, 0, 0, 0);
-      float y[8][4];
+      float y[4][4];
       int rg = 0, d0 = 0, n0 = 0, v0 = 0;
 #pragma unroll 1
       while (rg < valid) {
@@ -850,7 +836,7 @@ __global__ void __launch_bounds__(kDual ? 640 : 512, 1)
         const int lo = beam_of(i0 + rg + n8) - b0 - n0, hi = beam_of(i0 + rg + n8 + 8) - b0 - n0;
         if (n0 == 0 && v0 == 0) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
+          for (int k = 0; k < 4; ++k)
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[k][e] = 0.f;
         }
@@ -868,10 +854,8 @@ __global__ void __launch_bounds__(kDual ? 640 : 512, 1)
           aw[e] = at & 1 ? bf16x2(0.f, head) : bf16x2(head, 0.f);
           ar[e] = at & 1 ? bf16x2(0.f, wt - head) : bf16x2(wt - head, 0.f);
         }
-        const uint32_t w[4][4] = {{vw[0].x, vw[0].y, vw[0].z, vw[0].w},
-                                  {vw[1].x, vw[1].y, vw[1].z, vw[1].w},
-                                  {vw[2].x, vw[2].y, vw[2].z, vw[2].w},
-                                  {vw[3].x, vw[3].y, vw[3].z, vw[3].w}};
+        const uint32_t w[4][2] = {
+            {vw[0].x, vw[0].y}, {vw[1].x, vw[1].y}, {vw[2].x, vw[2].y}, {vw[3].x, vw[3].y}};
         const int rg_now = rg, d_now = d0;
         v0 += 2;
         bool part_done = false;
@@ -881,7 +865,7 @@ __global__ void __launch_bounds__(kDual ? 640 : 512, 1)
           if (n0 > b_end - b0) {
             n0 = 0;
             part_done = true;
-            d0 += 64;
+            d0 += 32;
             if (d0 == D) {
               d0 = 0;
               rg += 16;
@@ -890,7 +874,7 @@ __global__ void __launch_bounds__(kDual ? 640 : 512, 1)
         }
         if (rg < valid) load(rg, d0, n0, v0);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 2; ++k) {
           const uint32_t e0 = __byte_perm(w[0][k], w[1][k], 0x5410);
           const uint32_t e1 = __byte_perm(w[2][k], w[3][k], 0x5410);
           const uint32_t o0 = __byte_perm(w[0][k], w[1][k], 0x7632);
@@ -905,13 +889,13 @@ __global__ void __launch_bounds__(kDual ? 640 : 512, 1)
         // through their zero weights: such a part is added up row by row.
         float all = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) all += (y[k][0] + y[k][1]) + (y[k][2] + y[k][3]);
+        for (int k = 0; k < 4; ++k) all += (y[k][0] + y[k][1]) + (y[k][2] + y[k][3]);
         if (__any_sync(0xFFFFFFFFu, !(fabsf(all) < 3.0e38f))) {
 #pragma unroll 1
           for (int lr = rg_now; lr < min(rg_now + 16, valid); ++lr) {
             const uint32_t at = __shfl_sync(0xFFFFFFFFu, off, lr);
 #pragma unroll 1
-            for (int d = d_now + lane; d < d_now + 64; d += 32) {
+            for (int d = d_now + lane; d < d_now + 32; d += 32) {
               float z = 0.f;
 #pragma unroll 1
               for (int v = 0; v < a.level; ++v) {
@@ -923,18 +907,15 @@ __global__ void __launch_bounds__(kDual ? 640 : 512, 1)
             }
           }
         } else {
-          // This lane: columns 16 c .. + 15 of the part's rows n8 and + 8.
+          // This lane: columns 8 c .. + 7 of the part's rows n8 and n8 + 8.
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             const int lr = rg_now + n8 + half * 8, e = half * 2;
             const uint32_t at = __shfl_sync(0xFFFFFFFFu, off, lr);
-            if (lr < valid) {
-              uint4* dst = reinterpret_cast<uint4*>(out + at + d_now + c * 16);
-              dst[0] = make_uint4(bf16x2(y[0][e], y[1][e]), bf16x2(y[2][e], y[3][e]),
-                                  bf16x2(y[4][e], y[5][e]), bf16x2(y[6][e], y[7][e]));
-              dst[1] = make_uint4(bf16x2(y[0][e + 1], y[1][e + 1]), bf16x2(y[2][e + 1], y[3][e + 1]),
-                                  bf16x2(y[4][e + 1], y[5][e + 1]), bf16x2(y[6][e + 1], y[7][e + 1]));
-            }
+            if (lr < valid)
+              *reinterpret_cast<uint4*>(out + at + d_now + c * 8) =
+                  make_uint4(bf16x2(y[0][e], y[1][e]), bf16x2(y[2][e], y[3][e]),
+                             bf16x2(y[0][e + 1], y[1][e + 1]), bf16x2(y[2][e + 1], y[3][e + 1]));
           }
         }
       }
@@ -1071,10 +1052,9 @@ __global__ void __launch_bounds__(kDual ? 640 : 512, 1)
     }
     for (int w = first_unit; ok && w < a.units; w += stride) {
       const bool have_next = w + stride < a.units;
-      Unit nx = u;
       if (have_next) {
         // The next unit's q on its way to L2.
-        nx = unit_of<kDual>(a, w + stride, rank);
+        const Unit nx = unit_of<kDual>(a, w + stride, rank);
         if (lane < rows_in(nx))
           for (int c = 0; c < D; c += 64)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(a.q + row_base(nx, a.q_stride) +
@@ -1086,7 +1066,11 @@ __global__ void __launch_bounds__(kDual ? 640 : 512, 1)
         if (rank == 0) attend_path(u, dead);
       }
       // The next unit's Q comes in once this one's last products are done.
-      if (have_next) load_q(nx, steps_of<kDual>(u, tile) > 0);
+      Unit nx = u;
+      if (have_next) {
+        nx = unit_of<kDual>(a, w + stride, rank);
+        load_q(nx, steps_of<kDual>(u, tile) > 0);
+      }
       if constexpr (kSplit) {
         // Partial rows go where Q and the ring are: both streams end first, and
         // every warp has read Q. (One unit only: all of these warps come here.)
