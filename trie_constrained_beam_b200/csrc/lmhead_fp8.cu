@@ -43,21 +43,18 @@ struct Fp8Args {
   uint32_t* status;
 };
 
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                     uint32_t* status) {
-  return bounded_wait(bar, parity, abort, status, kStatusTimeout);
-}
-
 // ------------------------------------------------------------ many rows
-// Persistent over 128 x 256 tiles. Warp 0 loads (TMA), warp 1 issues MMAs, warps
-// 2-9 are the epilogue: the warp pair of a TMEM lane quarter takes 128 columns
-// each (one scale block), 128 fp32 registers per thread.
+// Persistent over 128 x 256 tiles. Two warp groups are the epilogue, each on 128
+// columns (one scale block) of a tile: 128 fp32 sums per thread. The third issues
+// (warp 8: TMA, warp 9: MMA). A block's MMAs take 512 cycles, and so at least does
+// its way out: 128 KB of TMEM reads and 32K FMAs per SM; the epilogue keeps three
+// loads of 32 columns in turn, so that neither waits for the other.
 constexpr int kTileM = 128;
 constexpr int kTileN = 256;
 constexpr int kStages = 4;
 constexpr int kABytes = kTileM * kBlock;
 constexpr int kStageBytes = (kTileM + kTileN) * kBlock;  // 48 KiB
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
 constexpr int kChunk = 128;                              // bytes of a row per store chunk
 constexpr int kStore = kEpiWarps * 32 * kChunk;          // 32 KiB
@@ -98,65 +95,71 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc(tmem_slot, 512);
+  if (warp == 9) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  constexpr uint32_t tmem = 0u;  // all 512 columns: they begin at column 0
 
-  if (warp == 0) {
-    if (lane == 0) {
-      prefetch_map(&map_h);
-      prefetch_map(&map_w);
-      uint32_t it = 0;
-      for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-        const int nt = t / m_tiles, mt = t - nt * m_tiles;
-        for (int k = 0; k < a.nb; ++k, ++it) {
-          const int s = static_cast<int>(it % kStages);
-          if (it >= static_cast<uint32_t>(kStages) &&
-              !wait(&empty[s], ((it / kStages) - 1) & 1u, abort_flag, a.status))
-            goto loaded;
-          uint8_t* st = smem + s * kStageBytes;
-          mbar_arrive_expect_tx(&full[s], kStageBytes);
-          tma_load_2d(st, &map_h, k * kBlock, mt * kTileM, &full[s]);
-          tma_load_2d(st + kABytes, &map_w, k * kBlock, nt * kTileN, &full[s]);
-        }
-      }
-    loaded:
-      for (uint32_t j = it > static_cast<uint32_t>(kStages) ? it - kStages : 0u; j < it; ++j)
-        drain_wait(&full[j % kStages], (j / kStages) & 1u);
-    }
-  } else if (warp == 1) {
-    if (elect_one()) {
-      uint32_t it = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-        for (int k = 0; k < a.nb; ++k, ++it) {
-          const int s = static_cast<int>(it % kStages);
-          const uint32_t ab = it & 1u;
-          if ((it >= 2 && !wait(&acc_empty[ab], ((it >> 1) - 1) & 1u, abort_flag, a.status)) ||
-              !wait(&full[s], (it / kStages) & 1u, abort_flag, a.status)) {
-            ok = false;
-            break;
+  // Registers: 384 threads start with 168 each; 232 + 232 + 40 = 3 * 168.
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 8) {
+      if (lane == 0) {
+        prefetch_map(&map_h);
+        prefetch_map(&map_w);
+        uint32_t it = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+          const int nt = t / m_tiles, mt = t - nt * m_tiles;
+          for (int k = 0; k < a.nb; ++k, ++it) {
+            const uint32_t s = it % kStages;
+            if (it >= kStages && !lane_wait(&empty[s], it / kStages - 1, abort_flag, a.status)) {
+              ok = false;
+              break;
+            }
+            uint8_t* st = smem + s * kStageBytes;
+            mbar_arrive_expect_tx(&full[s], kStageBytes);
+            tma_load_2d(st, &map_h, k * kBlock, mt * kTileM, &full[s]);
+            tma_load_2d(st + kABytes, &map_w, k * kBlock, nt * kTileN, &full[s]);
           }
-          tc_fence_after();
-          const uint32_t sa = smem_addr(smem + s * kStageBytes);
-          const uint32_t sb = sa + kABytes;
-#pragma unroll
-          for (int kk = 0; kk < kBlock / 32; ++kk)
-            umma_f8(tmem + ab * kTileN, smem_desc(sa + kk * 32), smem_desc(sb + kk * 32),
-                    idesc_f8(kTileN), kk > 0 ? 1u : 0u);
-          umma_commit(&empty[s]);
-          umma_commit(&acc_full[ab]);
         }
+        for (uint32_t j = it > kStages ? it - kStages : 0u; j < it; ++j)
+          drain_wait(&full[j % kStages], (j / kStages) & 1u);
       }
-      umma_commit(drain);
-      drain_wait(drain, 0u);
+    } else if (warp == 9) {
+      if (elect_one()) {
+        uint32_t it = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+          for (int k = 0; k < a.nb; ++k, ++it) {
+            const uint32_t s = it % kStages, ab = it & 1u;
+            if (!lane_wait(&full[s], it / kStages, abort_flag, a.status) ||
+                (it >= 2 && !lane_wait(&acc_empty[ab], (it >> 1) - 1, abort_flag, a.status))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t da = smem_desc(smem_addr(smem + s * kStageBytes));
+            const uint64_t db = smem_desc(smem_addr(smem + s * kStageBytes + kABytes));
+#pragma unroll
+            for (int kk = 0; kk < kBlock / 32; ++kk)
+              umma_f8(tmem + ab * kTileN, da + kk * 2, db + kk * 2, idesc_f8(kTileN),
+                      kk > 0 ? 1u : 0u);
+            umma_commit(&acc_full[ab]);
+            umma_commit(&empty[s]);
+          }
+        }
+        umma_commit(drain);
+        drain_wait(drain, 0u);
+      }
     }
+    __syncwarp();
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const int quarter = warp & 3;       // TMEM lanes 32 * quarter .. + 31
-    const int half = (warp - 2) >> 2;   // columns 128 * half .. + 127 of the tile
-    uint8_t* chunk = store + (warp - 2) * 32 * kChunk;
+    const int half = warp >> 2;         // columns 128 * half .. + 127 of the tile
+    uint8_t* chunk = store + warp * 32 * kChunk;
     uint32_t it = 0;
     bool ok = true;
     for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
@@ -170,6 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int e = 0; e < 64; ++e) acc[e] = zero;
       float s = sa[0] * sw[0];
+#pragma unroll 1
       for (int k = 0; k < a.nb; ++k, ++it) {
         const uint32_t ab = it & 1u;
         const uint64_t s2 = pack_f32x2(s, s);
@@ -181,21 +185,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t taddr = tmem + ab * kTileN + half * kBlock +
                                (static_cast<uint32_t>(quarter * 32) << 16);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t v[32];
-          tmem_ld32(taddr + j * 32, v);
-          if (j == 3) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[ab]);
-          }
+        uint32_t v0[32], v1[32], v2[32];
+        auto add = [&](int j, const uint32_t (&v)[32]) {
 #pragma unroll
           for (int e = 0; e < 16; ++e)
             acc[j * 16 + e] =
                 fma_f32x2(pack_f32x2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), s2,
                           acc[j * 16 + e]);
-        }
+        };
+        tmem_ld32_async(taddr, v0);
+        tmem_ld32_async(taddr + 32, v1);
+        tmem_wait_ld32(v0);
+        tmem_wait_ld32(v1);
+        tmem_ld32_async(taddr + 64, v2);
+        add(0, v0);
+        tmem_ld32_async(taddr + 96, v0);
+        add(1, v1);
+        tmem_wait_ld32(v2);
+        tmem_wait_ld32(v0);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[ab]);
+        add(2, v2);
+        add(3, v0);
       }
       if (!ok) break;
       // 128-byte pieces of the warp's 32 rows through shared memory (16-byte
@@ -249,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_free(tmem, 512);
+  if (warp == 9) tmem_free(tmem, 512);
 }
 
 // ------------------------------------------------------------ few rows
@@ -314,7 +326,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
       int i = 0;
       for (; i < n; ++i) {
         const int s = i % stages;
-        if (i >= stages && !wait(&empty[s], ((i / stages) - 1) & 1u, &abort_flag, a.status)) break;
+        if (i >= stages && !lane_wait(&empty[s], i / stages - 1, &abort_flag, a.status)) break;
         uint8_t* st = smem + s * P::kStage;
         mbar_arrive_expect_tx(&full[s], P::kStage);
         tma_load_2d(st, &map_w, (kb0 + i) * kBlock, tile * kTileM, &full[s]);
@@ -328,8 +340,8 @@ __global__ void __launch_bounds__(kRowThreads, 1)
       for (int i = 0; i < n; ++i) {
         const int s = i % stages, ab = i % P::kAcc;
         if ((i >= P::kAcc &&
-             !wait(&acc_empty[ab], ((i / P::kAcc) - 1) & 1u, &abort_flag, a.status)) ||
-            !wait(&full[s], (i / stages) & 1u, &abort_flag, a.status))
+             !lane_wait(&acc_empty[ab], i / P::kAcc - 1, &abort_flag, a.status)) ||
+            !lane_wait(&full[s], i / stages, &abort_flag, a.status))
           break;
         tc_fence_after();
         const uint32_t sw = smem_addr(smem + s * P::kStage);
