@@ -26,7 +26,6 @@ namespace {
 using namespace dev;
 
 constexpr int kBlock = SIDBEAM_FP8_BLOCK;  // 128 e4m3: 128 bytes, one swizzle row
-constexpr float kZero = 0.f;
 
 // Instruction descriptor of kind::f8f6f4: fp32 accumulator, e4m3 A and B (format
 // 0), both K-major, M = 128.
@@ -168,15 +167,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n0 = nt * kTileN + half * kBlock;
       const float* sa = a.sa + static_cast<int64_t>(min(row, a.M - 1)) * a.nb;
       const float* sw = a.sw + static_cast<int64_t>(min(n0, a.V - 1) / kBlock) * a.nb;
-      uint64_t acc[64];
-      const uint64_t zero = pack_f32x2(kZero, kZero);
+      float acc[128];
 #pragma unroll
-      for (int e = 0; e < 64; ++e) acc[e] = zero;
+      for (int e = 0; e < 128; ++e) acc[e] = 0.f;
       float s = sa[0] * sw[0];
 #pragma unroll 1
       for (int k = 0; k < a.nb; ++k, ++it) {
         const uint32_t ab = it & 1u;
-        const uint64_t s2 = pack_f32x2(s, s);
+        const float f = s;
         if (k + 1 < a.nb) s = sa[k + 1] * sw[k + 1];
         if (!warp_wait(&acc_full[ab], it >> 1, abort_flag, a.status)) {
           ok = false;
@@ -188,10 +186,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t v0[32], v1[32], v2[32];
         auto add = [&](int j, const uint32_t (&v)[32]) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            acc[j * 16 + e] =
-                fma_f32x2(pack_f32x2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), s2,
-                          acc[j * 16 + e]);
+          for (int e = 0; e < 32; ++e)
+            acc[j * 32 + e] = fmaf(__uint_as_float(v[e]), f, acc[j * 32 + e]);
         };
         tmem_ld32_async(taddr, v0);
         tmem_ld32_async(taddr + 32, v1);
@@ -219,15 +215,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
           uint4 w;
-          float f[8];
           if constexpr (sizeof(T) == 4) {
-            unpack_f32x2(acc[j * 16 + u * 2], f[0], f[1]);
-            unpack_f32x2(acc[j * 16 + u * 2 + 1], f[2], f[3]);
+            const float* f = acc + j * 32 + u * 4;
             w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
                            __float_as_uint(f[3]));
           } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) unpack_f32x2(acc[j * 32 + u * 4 + e], f[2 * e], f[2 * e + 1]);
+            const float* f = acc + j * 64 + u * 8;
             w = make_uint4(bf16x2(f[0], f[1]), bf16x2(f[2], f[3]), bf16x2(f[4], f[5]),
                            bf16x2(f[6], f[7]));
           }
