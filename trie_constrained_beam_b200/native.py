@@ -344,34 +344,39 @@ def fused_lmhead_step(trie, step, hidden, w_sid, parent_scores, parent_nodes, R,
     _check(rc)
 
 
-def _need(t, name, dtype, index, shape=None):
-    """Checks a tensor argument of device `index`; returns its address. ``shape``:
-    that of a contiguous tensor."""
-    if t is None:
-        raise ValueError(f"{name} is missing")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} dtype {t.dtype} is not {dtype}")
-    at = t.get_device()
-    if at != index or at < 0:
-        raise ValueError(f"{name} is on {t.device}, not on CUDA device {max(index, 0)}")
-    if shape is not None and (t.shape != shape or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous tensor of shape {shape}, "
-                         f"got {tuple(t.shape)} with strides {t.stride()}")
-    return t.data_ptr()
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
-def _workspace(t, index):
-    """(address, bytes) of a workspace of any element type."""
-    if t.get_device() != index:
-        raise ValueError(f"workspace is on {t.device}, not on CUDA device {index}")
-    return t.data_ptr(), t.nbytes
+def _refuse(index, *args):
+    """Raises for the first argument (tensor, name, dtype, shape of a contiguous
+    tensor or None) that does not fit a call on CUDA device `index`."""
+    for t, name, dtype, shape in args:
+        if t is None:
+            if name in ("residual", "residual_out"):
+                continue
+            raise ValueError(f"{name} is missing")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} dtype {t.dtype} is not {dtype}")
+        at = t.get_device()
+        if at != index or at < 0:
+            raise ValueError(f"{name} is on {t.device}, not on CUDA device {max(index, 0)}")
+        if shape is not None and (t.shape != shape or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}, "
+                             f"got {tuple(t.shape)} with strides {t.stride()}")
+    raise ValueError("arguments do not fit")
+
+
+def _fits(t, dtype, index, shape):
+    """Whether t is a contiguous tensor of that type, device and shape."""
+    return (t.dtype is dtype and t.get_device() == index and t.shape == shape
+            and t.is_contiguous())
 
 
 def _run_on(index, stream, fn, *args):
     """Calls a C entry on CUDA device `index`: on `stream`, or on that device's
     current stream."""
-    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    if index == torch._C._cuda_getDevice():
+    s = _raw_stream(index) if stream is None else stream.cuda_stream
+    if index == _current_device():
         rc = fn(*args, s)
     else:
         with torch.cuda.device(index):
@@ -388,12 +393,19 @@ def residual_rmsnorm_fp8(x, residual, weight, eps, residual_out, hidden_q, hidde
     (or None) receives h in bf16 and may be x or residual itself."""
     shape = M, d = x.shape
     at = x.get_device()
-    _run_on(at, stream, load().residual_rmsnorm_fp8, _need(x, "x", _BF16, at, shape),
-            None if residual is None else _need(residual, "residual", _BF16, at, shape),
-            _need(weight, "weight", _BF16, at, (d,)), eps, M, d,
-            None if residual_out is None else _need(residual_out, "residual_out", _BF16, at, shape),
-            _need(hidden_q, "hidden_q", _E4M3, at, shape),
-            _need(hidden_scale, "hidden_scale", _F32, at, (M, -(-d // FP8_BLOCK))))
+    scales = (M, (d + FP8_BLOCK - 1) // FP8_BLOCK)
+    if not (at >= 0 and x.dtype is _BF16 and x.is_contiguous()
+            and (residual is None or _fits(residual, _BF16, at, shape))
+            and _fits(weight, _BF16, at, (d,))
+            and (residual_out is None or _fits(residual_out, _BF16, at, shape))
+            and _fits(hidden_q, _E4M3, at, shape) and _fits(hidden_scale, _F32, at, scales)):
+        _refuse(at, (x, "x", _BF16, shape), (residual, "residual", _BF16, shape),
+                (weight, "weight", _BF16, (d,)), (residual_out, "residual_out", _BF16, shape),
+                (hidden_q, "hidden_q", _E4M3, shape), (hidden_scale, "hidden_scale", _F32, scales))
+    _run_on(at, stream, (_lib or load()).residual_rmsnorm_fp8, x.data_ptr(),
+            None if residual is None else residual.data_ptr(), weight.data_ptr(), eps, M, d,
+            None if residual_out is None else residual_out.data_ptr(), hidden_q.data_ptr(),
+            hidden_scale.data_ptr())
 
 
 def lmhead_quantize_fp8(w_sid, w_q, w_scale, stream=None):
@@ -401,9 +413,13 @@ def lmhead_quantize_fp8(w_sid, w_q, w_scale, stream=None):
     w_q e4m3 [V][d], w_scale f32 [ceil(V/128)][ceil(d/128)]."""
     shape = V, d = w_sid.shape
     at = w_sid.get_device()
-    _run_on(at, stream, load().lmhead_quantize_fp8, _need(w_sid, "w_sid", _BF16, at, shape), V, d,
-            _need(w_q, "w_q", _E4M3, at, shape),
-            _need(w_scale, "w_scale", _F32, at, (-(-V // FP8_BLOCK), -(-d // FP8_BLOCK))))
+    scales = ((V + FP8_BLOCK - 1) // FP8_BLOCK, (d + FP8_BLOCK - 1) // FP8_BLOCK)
+    if not (at >= 0 and w_sid.dtype is _BF16 and w_sid.is_contiguous()
+            and _fits(w_q, _E4M3, at, shape) and _fits(w_scale, _F32, at, scales)):
+        _refuse(at, (w_sid, "w_sid", _BF16, shape), (w_q, "w_q", _E4M3, shape),
+                (w_scale, "w_scale", _F32, scales))
+    _run_on(at, stream, (_lib or load()).lmhead_quantize_fp8, w_sid.data_ptr(), V, d,
+            w_q.data_ptr(), w_scale.data_ptr())
 
 
 def lmhead_logits_fp8(hidden_q, hidden_scale, w_q, w_scale, out, workspace, stream=None):
@@ -412,7 +428,7 @@ def lmhead_logits_fp8(hidden_q, hidden_scale, w_q, w_scale, out, workspace, stre
     (fp32 accumulation). out f32 or bf16 [M][V], rows out.stride(0) apart."""
     M, d = hidden_q.shape
     V = w_q.shape[0]
-    nb = -(-d // FP8_BLOCK)
+    nb = (d + FP8_BLOCK - 1) // FP8_BLOCK
     at = hidden_q.get_device()
     dtype = _dtype_code(out)
     ld, col = out.stride()
@@ -420,13 +436,19 @@ def lmhead_logits_fp8(hidden_q, hidden_scale, w_q, w_scale, out, workspace, stre
         raise ValueError(f"out must be [{M}, {V}] with unit column stride, got "
                          f"{tuple(out.shape)} with strides {out.stride()}")
     if M <= 1:  # the stride of a single row means nothing: any aligned one serves
-        ld = -(-V // 8) * 8
-    _run_on(at, stream, load().lmhead_logits_fp8,
-            _need(hidden_q, "hidden_q", _E4M3, at, (M, d)),
-            _need(hidden_scale, "hidden_scale", _F32, at, (M, nb)),
-            _need(w_q, "w_q", _E4M3, at, (V, d)),
-            _need(w_scale, "w_scale", _F32, at, (-(-V // FP8_BLOCK), nb)), M, V, d,
-            _need(out, "out", out.dtype, at), dtype, ld, *_workspace(workspace, at))
+        ld = (V + 7) // 8 * 8
+    vb = (V + FP8_BLOCK - 1) // FP8_BLOCK
+    if not (at >= 0 and hidden_q.dtype is _E4M3 and hidden_q.is_contiguous()
+            and _fits(hidden_scale, _F32, at, (M, nb)) and _fits(w_q, _E4M3, at, (V, d))
+            and _fits(w_scale, _F32, at, (vb, nb)) and out.get_device() == at
+            and workspace.get_device() == at):
+        _refuse(at, (hidden_q, "hidden_q", _E4M3, (M, d)),
+                (hidden_scale, "hidden_scale", _F32, (M, nb)), (w_q, "w_q", _E4M3, (V, d)),
+                (w_scale, "w_scale", _F32, (vb, nb)), (out, "out", out.dtype, None),
+                (workspace, "workspace", workspace.dtype, None))
+    _run_on(at, stream, (_lib or load()).lmhead_logits_fp8, hidden_q.data_ptr(),
+            hidden_scale.data_ptr(), w_q.data_ptr(), w_scale.data_ptr(), M, V, d, out.data_ptr(),
+            dtype, ld, workspace.data_ptr(), workspace.nbytes)
 
 
 def beam_attention(q, k_cache, v_cache, cache_len, out, workspace, page_table=None, level=0,
@@ -468,21 +490,34 @@ def beam_attention(q, k_cache, v_cache, cache_len, out, workspace, page_table=No
     if n_pages == 1:
         page = page_size * token
     table, per, kb, vb, bp = None, 0, None, None, None
+    if not (at >= 0 and q.dtype is _BF16 and k_cache.dtype is _BF16 and v_cache.dtype is _BF16
+            and out.dtype is _BF16 and k_cache.get_device() == at and v_cache.get_device() == at
+            and out.get_device() == at and workspace.get_device() == at
+            and _fits(cache_len, _I32, at, (R,))):
+        _refuse(at, (q, "q", _BF16, None), (k_cache, "k_cache", _BF16, None),
+                (v_cache, "v_cache", _BF16, None), (cache_len, "cache_len", _I32, (R,)),
+                (out, "out", _BF16, None), (workspace, "workspace", workspace.dtype, None))
     if page_table is not None:
         per = page_table.shape[-1]
-        table = _need(page_table, "page_table", _I32, at, (R, per))
+        if not _fits(page_table, _I32, at, (R, per)):
+            _refuse(at, (page_table, "page_table", _I32, (R, per)))
+        table = page_table.data_ptr()
     if level > 0:
         for t, name in ((bp_parent, "bp_parent"), (k_beam, "k_beam"), (v_beam, "v_beam")):
             if t is None or t.shape[0] < level:
                 raise ValueError(f"{name} holds fewer than {level} levels")
-        bp = _need(bp_parent, "bp_parent", _I32, at, (bp_parent.shape[0], R, B))
-        kb = _need(k_beam, "k_beam", _BF16, at, (k_beam.shape[0], rows, Hkv, D))
-        vb = _need(v_beam, "v_beam", _BF16, at, (v_beam.shape[0], rows, Hkv, D))
-    _run_on(at, stream, load().beam_attention, _need(q, "q", _BF16, at), q_row,
-            _need(k_cache, "k_cache", _BF16, at), _need(v_cache, "v_cache", _BF16, at), page, token,
-            n_pages, page_size, table, per, _need(cache_len, "cache_len", _I32, at, (R,)), level,
-            bp, kb, vb, R, B, H, Hkv, D, D ** -0.5 if scale is None else scale,
-            _need(out, "out", _BF16, at), o_row, *_workspace(workspace, at))
+        links, beams = (bp_parent.shape[0], R, B), (rows, Hkv, D)
+        if not (_fits(bp_parent, _I32, at, links)
+                and _fits(k_beam, _BF16, at, (k_beam.shape[0], *beams))
+                and _fits(v_beam, _BF16, at, (v_beam.shape[0], *beams))):
+            _refuse(at, (bp_parent, "bp_parent", _I32, links),
+                    (k_beam, "k_beam", _BF16, (k_beam.shape[0], *beams)),
+                    (v_beam, "v_beam", _BF16, (v_beam.shape[0], *beams)))
+        bp, kb, vb = bp_parent.data_ptr(), k_beam.data_ptr(), v_beam.data_ptr()
+    _run_on(at, stream, (_lib or load()).beam_attention, q.data_ptr(), q_row, k_cache.data_ptr(),
+            v_cache.data_ptr(), page, token, n_pages, page_size, table, per, cache_len.data_ptr(),
+            level, bp, kb, vb, R, B, H, Hkv, D, D ** -0.5 if scale is None else scale,
+            out.data_ptr(), o_row, workspace.data_ptr(), workspace.nbytes)
 
 
 def sidbeam_get_device_status(workspace, stream=None) -> int:
