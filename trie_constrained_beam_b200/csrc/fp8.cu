@@ -188,9 +188,6 @@ __global__ void __launch_bounds__(kQuantThreads)
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Rows from which a warp per row fills the GPU; fewer rows take a CTA each.
-constexpr int kWarpRows = 1184;  // 8 rows per SM
-
 template <int T>
 void launch_rmsnorm(int k, const void* x, const void* residual, const void* weight, float eps,
                     int M, int d, void* residual_out, void* q, float* scale, cudaStream_t s) {
@@ -233,9 +230,12 @@ extern "C" int residual_rmsnorm_fp8(const void* x, const void* residual, const v
     return set_error(SIDBEAM_ERR_ALIGNMENT, "residual_rmsnorm_fp8: pointers must be 16-byte aligned");
   const int chunks = d / 8;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (M >= kWarpRows && chunks <= 32 * 8)
+  if (chunks <= 64)
     launch_rmsnorm<32>((chunks + 31) / 32, x, residual, weight, eps, M, d, residual_out, hidden_q,
                        hidden_scale, s);
+  else if (chunks <= 128 * 8)
+    launch_rmsnorm<128>((chunks + 127) / 128, x, residual, weight, eps, M, d, residual_out,
+                        hidden_q, hidden_scale, s);
   else
     launch_rmsnorm<256>((chunks + 255) / 256, x, residual, weight, eps, M, d, residual_out,
                         hidden_q, hidden_scale, s);

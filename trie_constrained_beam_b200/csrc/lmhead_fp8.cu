@@ -43,35 +43,42 @@ struct Fp8Args {
 };
 
 // ------------------------------------------------------------ many rows
-// Persistent over 128 x 256 tiles. Two warp groups are the epilogue, each on 128
-// columns (one scale block) of a tile: 128 fp32 sums per thread. The third issues
+// Persistent over tiles of 128 rows x kTileN codes. Two warp groups are the epilogue,
+// each on half of a tile's columns: 128 (or 64) fp32 sums per thread. The third issues
 // (warp 8: TMA, warp 9: MMA). A block's MMAs take 512 cycles, and so at least does
 // its way out: 128 KB of TMEM reads and 32K FMAs per SM; the epilogue keeps three
 // loads of 32 columns in turn, so that neither waits for the other.
 constexpr int kTileM = 128;
-constexpr int kTileN = 256;
-constexpr int kStages = 4;
 constexpr int kABytes = kTileM * kBlock;
-constexpr int kStageBytes = (kTileM + kTileN) * kBlock;  // 48 KiB
 constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
 constexpr int kChunk = 128;                              // bytes of a row per store chunk
 constexpr int kStore = kEpiWarps * 32 * kChunk;          // 32 KiB
-constexpr int kSmem = kStages * kStageBytes + kStore + 1024 + 256;
+template <int kTileN>
+struct GemmPlan {
+  static constexpr int kStages = kTileN == 256 ? 4 : 6;  // of 48 or 32 KiB
+  static constexpr int kStageBytes = (kTileM + kTileN) * kBlock;
+  static constexpr int kAccs = 512 / kTileN;             // TMEM accumulators
+  static constexpr int kCols = kTileN / 2;               // columns of an epilogue warp
+  static constexpr int kSmem = kStages * kStageBytes + kStore + 1024 + 256;
+};
 
-template <typename T>
+template <int kTileN, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_h,
                     const __grid_constant__ CUtensorMap map_w, const Fp8Args a) {
+  using P = GemmPlan<kTileN>;
+  constexpr int kStages = P::kStages, kStageBytes = P::kStageBytes, kAccs = P::kAccs;
+  constexpr int kCols = P::kCols;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* store = smem + kStages * kStageBytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(store + kStore);
   uint64_t* empty = full + kStages;
-  uint64_t* acc_full = empty + kStages;  // [2]
-  uint64_t* acc_empty = acc_full + 2;    // [2]
-  uint64_t* drain = acc_empty + 2;
+  uint64_t* acc_full = empty + kStages;  // [kAccs]
+  uint64_t* acc_empty = acc_full + kAccs;
+  uint64_t* drain = acc_empty + kAccs;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
 
@@ -86,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kAccs; ++b) {
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], kEpiWarps);
     }
@@ -132,9 +139,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
           for (int k = 0; k < a.nb; ++k, ++it) {
-            const uint32_t s = it % kStages, ab = it & 1u;
+            const uint32_t s = it % kStages, ab = it % kAccs;
             if (!lane_wait(&full[s], it / kStages, abort_flag, a.status) ||
-                (it >= 2 && !lane_wait(&acc_empty[ab], (it >> 1) - 1, abort_flag, a.status))) {
+                (it >= kAccs && !lane_wait(&acc_empty[ab], it / kAccs - 1, abort_flag, a.status))) {
               ok = false;
               break;
             }
@@ -157,31 +164,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const int quarter = warp & 3;       // TMEM lanes 32 * quarter .. + 31
-    const int half = warp >> 2;         // columns 128 * half .. + 127 of the tile
+    const int col0 = (warp >> 2) * kCols;  // first of its columns in the tile
     uint8_t* chunk = store + warp * 32 * kChunk;
     uint32_t it = 0;
     bool ok = true;
     for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
       const int nt = t / m_tiles, mt = t - nt * m_tiles;
       const int row = mt * kTileM + quarter * 32 + lane;
-      const int n0 = nt * kTileN + half * kBlock;
+      const int n0 = nt * kTileN + col0;
       const float* sa = a.sa + static_cast<int64_t>(min(row, a.M - 1)) * a.nb;
       const float* sw = a.sw + static_cast<int64_t>(min(n0, a.V - 1) / kBlock) * a.nb;
-      float acc[128];
+      float acc[kCols];
 #pragma unroll
-      for (int e = 0; e < 128; ++e) acc[e] = 0.f;
+      for (int e = 0; e < kCols; ++e) acc[e] = 0.f;
       float s = sa[0] * sw[0];
 #pragma unroll 1
       for (int k = 0; k < a.nb; ++k, ++it) {
-        const uint32_t ab = it & 1u;
+        const uint32_t ab = it % kAccs;
         const float f = s;
         if (k + 1 < a.nb) s = sa[k + 1] * sw[k + 1];
-        if (!warp_wait(&acc_full[ab], it >> 1, abort_flag, a.status)) {
+        if (!warp_wait(&acc_full[ab], it / kAccs, abort_flag, a.status)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t taddr = tmem + ab * kTileN + half * kBlock +
+        const uint32_t taddr = tmem + ab * kTileN + col0 +
                                (static_cast<uint32_t>(quarter * 32) << 16);
         uint32_t v0[32], v1[32], v2[32];
         auto add = [&](int j, const uint32_t (&v)[32]) {
@@ -189,29 +196,38 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 32; ++e)
             acc[j * 32 + e] = fmaf(__uint_as_float(v[e]), f, acc[j * 32 + e]);
         };
+        auto release = [&] {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_empty[ab]);
+        };
         tmem_ld32_async(taddr, v0);
         tmem_ld32_async(taddr + 32, v1);
         tmem_wait_ld32(v0);
         tmem_wait_ld32(v1);
-        tmem_ld32_async(taddr + 64, v2);
-        add(0, v0);
-        tmem_ld32_async(taddr + 96, v0);
-        add(1, v1);
-        tmem_wait_ld32(v2);
-        tmem_wait_ld32(v0);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&acc_empty[ab]);
-        add(2, v2);
-        add(3, v0);
+        if constexpr (kCols == 64) {
+          release();
+          add(0, v0);
+          add(1, v1);
+        } else {
+          tmem_ld32_async(taddr + 64, v2);
+          add(0, v0);
+          tmem_ld32_async(taddr + 96, v0);
+          add(1, v1);
+          tmem_wait_ld32(v2);
+          tmem_wait_ld32(v0);
+          release();
+          add(2, v2);
+          add(3, v0);
+        }
       }
       if (!ok) break;
       // 128-byte pieces of the warp's 32 rows through shared memory (16-byte
       // units, unit u of row l at u ^ (l & 7)), so that global stores cover
       // whole lines.
-      constexpr int kCols = kChunk / static_cast<int>(sizeof(T));  // 32 fp32 or 64 bf16
+      constexpr int kPiece = kChunk / static_cast<int>(sizeof(T));  // 32 fp32 or 64 bf16
 #pragma unroll
-      for (int j = 0; j < kBlock / kCols; ++j) {
+      for (int j = 0; j < kCols / kPiece; ++j) {
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
           uint4 w;
@@ -233,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int l = p * 4 + (lane >> 3), u = lane & 7;
           const uint4 w = *reinterpret_cast<const uint4*>(chunk + l * kChunk + ((u ^ (l & 7)) << 4));
           const int r = mt * kTileM + quarter * 32 + l;
-          const int c = n0 + j * kCols + u * kUnit;
+          const int c = n0 + j * kPiece + u * kUnit;
           if (r < a.M) {
             T* o = static_cast<T*>(a.out) + static_cast<int64_t>(r) * a.ld + c;
             if (c + kUnit <= a.V) {
@@ -268,7 +284,7 @@ constexpr int kRowThreads = 192;  // TMA warp, MMA warp, 4 epilogue warps
 template <int NB>
 struct RowPlan {
   static constexpr int kStage = (kTileM + NB) * kBlock;
-  static constexpr int kAcc = NB >= 128 ? 4 : 8;  // TMEM accumulators of NB columns
+  static constexpr int kAcc = 8;                      // TMEM accumulators of NB columns
   static constexpr int kTmemCols = NB * kAcc < 32 ? 32 : NB * kAcc;
 };
 
@@ -407,11 +423,26 @@ __global__ void __launch_bounds__(kRowThreads, 1)
   }
   cluster_sync();
   if (warp >= 2 && c < a.V) {
+    // Eight rows' parts in flight at a time (a remote load takes long).
     const int rows = min(NB, a.M - m0);
-    for (int j = rank; j < rows; j += split) {
-      float z = 0.f;
-      for (int p = 0; p < split; ++p) z += ld_peer(peer_addr(&part[j * 128 + c_local], p));
-      out[static_cast<int64_t>(m0 + j) * a.ld] = static_cast<T>(z);
+    for (int j0 = rank; j0 < rows; j0 += 8 * split) {
+      float z[8] = {};
+#pragma unroll 2
+      for (int p = 0; p < split; ++p) {
+        const uint32_t at = peer_addr(&part[c_local], p);
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int j = j0 + e * split;
+          v[e] = j < rows ? ld_peer(at + j * 512) : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] += v[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (j0 + e * split < rows)
+          out[static_cast<int64_t>(m0 + j0 + e * split) * a.ld] = static_cast<T>(z[e]);
     }
   }
   cluster_sync();  // no CTA leaves while another still reads its part
@@ -446,18 +477,18 @@ cudaError_t opt_in(K kernel, int smem, bool (&done)[64]) {
   return e;
 }
 
-template <typename T>
+template <int kTileN, typename T>
 int launch_gemm(const void* h, const void* w, const Fp8Args& a, int d, cudaStream_t stream) {
   CUtensorMap mh, mw;
   if (!make_map(&mh, h, a.M, d, kTileM) || !make_map(&mw, w, a.V, d, kTileN))
     return set_error(SIDBEAM_ERR_CUDA, "lmhead_logits_fp8: tensor map encoding failed");
   static bool done[64] = {};
-  cudaError_t e = opt_in(fp8_gemm_kernel<T>, kSmem, done);
+  cudaError_t e = opt_in(fp8_gemm_kernel<kTileN, T>, GemmPlan<kTileN>::kSmem, done);
   if (e != cudaSuccess) return cuda_error(e, "lmhead_logits_fp8: cudaFuncSetAttribute");
   const int64_t tiles =
       static_cast<int64_t>((a.M + kTileM - 1) / kTileM) * ((a.V + kTileN - 1) / kTileN);
   const int grid = static_cast<int>(std::min<int64_t>(tiles, device_sm_count()));
-  fp8_gemm_kernel<T><<<grid, kThreads, kSmem, stream>>>(mh, mw, a);
+  fp8_gemm_kernel<kTileN, T><<<grid, kThreads, GemmPlan<kTileN>::kSmem, stream>>>(mh, mw, a);
   e = cudaGetLastError();
   return e == cudaSuccess ? SIDBEAM_OK : cuda_error(e, "lmhead_logits_fp8: launch");
 }
@@ -476,7 +507,9 @@ int launch_rows(const void* h, const void* w, const Fp8Args& a, int d, cudaStrea
   while (split < 8 && split * 2 <= a.nb && tiles * groups * split * 2 <= sms) split *= 2;
   const int n = (a.nb + split - 1) / split;
   const int table = n * NB * 4;
-  const int budget = 224 * 1024 - 1024 - table;
+  // More CTAs than SMs: two to an SM.
+  const int room = tiles * groups * split > sms ? 112 : 224;
+  const int budget = room * 1024 - 1024 - table;
   const int stages = std::max(2, std::min({8, n, budget / P::kStage}));
   const int smem = 1024 + std::max(stages * P::kStage + table, NB * 128 * 4);
   static bool done[64] = {};
@@ -503,9 +536,9 @@ template <typename T>
 int launch(const void* h, const void* w, const Fp8Args& a, int d, cudaStream_t stream) {
   if (a.M <= 16) return launch_rows<16, T>(h, w, a, d, stream);
   if (a.M <= 32) return launch_rows<32, T>(h, w, a, d, stream);
-  if (a.M <= 64) return launch_rows<64, T>(h, w, a, d, stream);
-  if (a.M <= 128) return launch_rows<128, T>(h, w, a, d, stream);
-  return launch_gemm<T>(h, w, a, d, stream);
+  const int64_t tiles = static_cast<int64_t>((a.M + kTileM - 1) / kTileM) * ((a.V + 255) / 256);
+  return 2 * tiles <= device_sm_count() ? launch_gemm<128, T>(h, w, a, d, stream)
+                                        : launch_gemm<256, T>(h, w, a, d, stream);
 }
 
 bool misaligned(const void* p, uintptr_t to) {
