@@ -393,10 +393,11 @@ int lmhead_logits_fp8(const void* hidden_q, const float* hidden_scale, const voi
  *   out[row][h] = sum_j softmax_j(scale * <q[row][h], k_j>) v_j
  * with the keys and values of head h / (H / Hkv). Products bf16 on the tensor
  * cores, scores, maxima, sums and the output's accumulation in fp32; the weights
- * are rounded to bf16 before they meet the cached values.
+ * of cached tokens are rounded to bf16 before they meet the values, the ancestors'
+ * share of a row once to bf16 on its way to the output.
  *  q            device bf16 [R*B][H][D]; a row starts q_row_stride elements after
- *               the one before (>= H*D, % 8 == 0; a slice of a wider projection
- *               is fine). Rows are request-major, row = r * B + b.
+ *               the one before (>= H*D, % 8 == 0, < 2^24; a slice of a wider
+ *               projection is fine). Rows are request-major, row = r * B + b.
  *  k_cache,     device bf16 [n_pages][page_size][Hkv][D]; page and token strides
  *  v_cache      in elements, both % 8 == 0 and the same for both arrays.
  *  page_table   device i32 [R][pages_per_request] of page numbers: token i of
@@ -415,26 +416,49 @@ int lmhead_logits_fp8(const void* hidden_q, const float* hidden_scale, const voi
  *               are then ignored).
  *  bp_parent    device i32 [level][R][B], the first `level` slices of a search's
  *               history. A row one of whose links lies outside [0, B) (bp_parent[0]:
- *               < 0) is a dead beam: its output is zero.
+ *               < 0) is a dead beam: its output is zero, whatever its q and its
+ *               own keys and values hold.
  *  k_beam,      device bf16 [level][R*B][Hkv][D]: the keys and values of the token
- *  v_beam       each beam chose at each level.
+ *  v_beam       each beam chose at each level; together less than 64 GiB each.
  *  R, B         requests and rows per request, B <= SIDBEAM_MAX_BEAM.
  *  H, Hkv, D    query heads, key/value heads (H % Hkv == 0, H / Hkv <= 128), head
  *               size 64 or 128.
  *  scale        finite; usually 1 / sqrt(D).
  *  out          device bf16 [R*B][H][D] with out_row_stride (as q_row_stride). A
  *               row that attends nothing (no token, level 0) is zero. Must not
- *               overlap the inputs.
+ *               overlap the inputs; rows are written more than once.
  *  workspace    device, >= 256 bytes, 256-byte aligned, zero-filled before first
- *               use (status word).
- * Pointers 16-byte aligned. Asynchronous on `stream`. Errors: INVALID_ARG,
- * ALIGNMENT, WORKSPACE, CUDA. */
-int beam_attention(const void* q, int64_t q_row_stride, const void* k_cache, const void* v_cache,
-                   int64_t page_stride, int64_t token_stride, int n_pages, int page_size,
-                   const int32_t* page_table, int pages_per_request, const int32_t* cache_len,
-                   int level, const int32_t* bp_parent, const void* k_beam, const void* v_beam,
-                   int R, int B, int H, int Hkv, int D, float scale, void* out,
-                   int64_t out_row_stride, void* workspace, size_t workspace_bytes, void* stream);
+ *               use (status word); calls in flight at once may share it.
+ * Pointers 16-byte aligned. Asynchronous on `stream`; the struct is read before
+ * the call returns. Errors: INVALID_ARG, ALIGNMENT, WORKSPACE, CUDA. */
+typedef struct {
+  const void* q;
+  int64_t q_row_stride;
+  const void* k_cache;
+  const void* v_cache;
+  int64_t page_stride;
+  int64_t token_stride;
+  int32_t n_pages;
+  int32_t page_size;
+  const int32_t* page_table;
+  const int32_t* cache_len;
+  const int32_t* bp_parent;
+  const void* k_beam;
+  const void* v_beam;
+  int32_t pages_per_request;
+  int32_t level;
+  int32_t R;
+  int32_t B;
+  int32_t H;
+  int32_t Hkv;
+  int32_t D;
+  float scale;
+  void* out;
+  int64_t out_row_stride;
+  void* workspace;
+  size_t workspace_bytes;
+} sidbeam_attention;
+int beam_attention(const sidbeam_attention* args, void* stream);
 
 /* ---------------------------------------------------------------- status
  * sidbeam_get_device_status -- synchronises `stream`, reads and clears the

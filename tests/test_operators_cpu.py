@@ -127,11 +127,38 @@ def _attention(lib, **kw):
              per=4, lens=0x5000, level=2, bp=0x6000, kb=0x7000, vb=0x8000, R=2, B=4, H=4, Hkv=2,
              D=128, scale=0.1, out=0x9000, os=512, work=0xA000, wsize=256)
     a.update(kw)
-    return lib.beam_attention(P(a["q"]), a["qs"], P(a["k"]), P(a["v"]), a["ps"], a["ts"],
-                              a["pages"], a["size"], P(a["table"]) if a["table"] else None,
-                              a["per"], P(a["lens"]), a["level"], P(a["bp"]), P(a["kb"]),
-                              P(a["vb"]), a["R"], a["B"], a["H"], a["Hkv"], a["D"], a["scale"],
-                              P(a["out"]), a["os"], P(a["work"]), a["wsize"], None)
+    from trie_constrained_beam_b200 import native
+    return lib.beam_attention(native._ATTENTION(
+        a["q"], a["qs"], a["k"], a["v"], a["ps"], a["ts"], a["pages"], a["size"],
+        a["table"] or 0, a["lens"], a["bp"], a["kb"], a["vb"], a["per"], a["level"], a["R"],
+        a["B"], a["H"], a["Hkv"], a["D"], a["scale"], a["out"], a["os"], a["work"], a["wsize"]),
+        None)
+
+
+def test_attention_struct_layout(tmp_path):
+    """The binding packs what a C compiler lays out."""
+    import os
+    import shutil
+    import struct
+    import subprocess
+    if shutil.which("gcc") is None:
+        pytest.skip("no C compiler")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stdio.h>\n#include "sidbeam.h"\n#define O(f) '
+                   '(int)offsetof(sidbeam_attention, f)\nint main(void) {\n'
+                   '  printf("%d %d %d %d %d %d", (int)sizeof(sidbeam_attention), O(page_table),'
+                   ' O(pages_per_request), O(scale), O(out), O(workspace_bytes)); return 0; }\n')
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", "-I", os.path.join(root, "include"), str(src), "-o", str(exe)],
+                   check=True)
+    got = [int(x) for x in subprocess.check_output([str(exe)]).split()]
+    fields = "PqPPqqiiPPPPPiiiiiiifPqPN"
+    ends = [struct.calcsize(fields[:k + 1]) for k in range(len(fields))]
+    start = lambda k: ends[k] - struct.calcsize(fields[k])  # noqa: E731
+    assert got == [struct.calcsize(fields), start(8), start(13), start(20), start(21), start(24)]
+    from trie_constrained_beam_b200 import native
+    assert len(native._ATTENTION(*([0] * 20 + [0.0] + [0] * 4))) == got[0]
 
 
 def test_attention_refusals(lib):

@@ -806,6 +806,11 @@ __global__ void __launch_bounds__(kDual ? 640 : 512, 1)
           x[v] = dead ? 0.f : ex2_approx(x[v] - mp);
           lp += x[v];
         }
+        // (A NaN goes on in lp; as a weight it would make its neighbours' part a
+        // slow one below.)
+        if (!(lp >= 0.f))
+#pragma unroll 1
+          for (int v = 0; v < a.level; ++v) x[v] = 0.f;
       }
       __syncwarp();
       // ---- values: parts of 16 rows by 32 columns, in rounds of 8 beams x 2 levels,
@@ -953,10 +958,11 @@ __global__ void __launch_bounds__(kDual ? 640 : 512, 1)
         if (kDual || s == 0) st_a = got; else st_b = got;
       }
       tc_fence_after();
-      // One reference for all sources of the row. (l > 0 is false for NaN, which
-      // the q of a dead row may lead to.)
-      const bool has_a = st_a.y > 0.f && !dead, has_b = st_b.y > 0.f && !dead;
-      const bool has_p = lp > 0.f && !dead;
+      // One reference for all sources of the row that have keys (l is 0 without,
+      // and NaN where the row's scores are: that reaches the output, except for
+      // the q of a dead row).
+      const bool has_a = !(st_a.y <= 0.f) && !dead, has_b = !(st_b.y <= 0.f) && !dead;
+      const bool has_p = !(lp <= 0.f) && !dead;
       const float top = fmaxf(fmaxf(has_a ? st_a.x : kNegInf, has_b ? st_b.x : kNegInf),
                               has_p ? mp : kNegInf);
       const float ref = top > kNegInf ? top : 0.f;
@@ -966,7 +972,7 @@ __global__ void __launch_bounds__(kDual ? 640 : 512, 1)
       const float sum = f0 * st_a.y + f1 * st_b.y + fp * lp;
       const float total = has_a || has_b || has_p ? sum : 0.f;
       if constexpr (!kSplit) {
-        const float inv = total > 0.f ? 1.f / total : 0.f;
+        const float inv = total == 0.f ? 0.f : 1.f / total;
         f0 *= inv;
         f1 *= inv;
         fp *= inv;
@@ -979,7 +985,7 @@ __global__ void __launch_bounds__(kDual ? 640 : 512, 1)
       const int sa = kDual ? tile : 0;
       const bool read_a = valid > 0 && steps_of<kDual>(u, sa) > 0;
       const bool read_b = !kDual && valid > 0 && steps_of<kDual>(u, 1) > 0;
-      const bool with_path = kPath && fp > 0.f && lane < valid;
+      const bool with_path = kPath && has_p && lane < valid;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint4 pw[4];
@@ -1113,7 +1119,7 @@ __global__ void __launch_bounds__(kDual ? 640 : 512, 1)
           o.w = fmaf(wp, v.w, o.w);
         }
       }
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
       const int ii = u.row0 + i, b = ii / a.G, h = u.g * a.G + (ii - b * a.G);
       if (lane < D / 4)
         *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(u.r) * a.B + b) * a.out_stride +
@@ -1219,14 +1225,11 @@ bool misaligned(const void* p, uintptr_t to) {
 
 using namespace sidbeam;
 
-extern "C" int beam_attention(const void* q, int64_t q_row_stride, const void* k_cache,
-                              const void* v_cache, int64_t page_stride, int64_t token_stride,
-                              int n_pages, int page_size, const int32_t* page_table,
-                              int pages_per_request, const int32_t* cache_len, int level,
-                              const int32_t* bp_parent, const void* k_beam, const void* v_beam,
-                              int R, int B, int H, int Hkv, int D, float scale, void* out,
-                              int64_t out_row_stride, void* workspace, size_t workspace_bytes,
-                              void* stream) {
+extern "C" int beam_attention(const sidbeam_attention* args, void* stream) {
+  if (!args) return set_error(SIDBEAM_ERR_INVALID_ARG, "beam_attention: NULL arguments");
+  const auto [q, q_row_stride, k_cache, v_cache, page_stride, token_stride, n_pages, page_size,
+              page_table, cache_len, bp_parent, k_beam, v_beam, pages_per_request, level, R, B, H,
+              Hkv, D, scale, out, out_row_stride, workspace, workspace_bytes] = *args;
   if (!q || !k_cache || !v_cache || !cache_len || !out)
     return set_error(SIDBEAM_ERR_INVALID_ARG, "beam_attention: NULL pointer argument");
   if (R < 1 || B < 1 || B > SIDBEAM_MAX_BEAM || static_cast<int64_t>(R) * B > 0x7FFFFFFFll)

@@ -191,7 +191,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 template <int T>
 void launch_rmsnorm(int k, const void* x, const void* residual, const void* weight, float eps,
                     int M, int d, void* residual_out, void* q, float* scale, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(T == 32 ? (M + 3) / 4 : M));
+  const dim3 grid(static_cast<unsigned>(T == 32 ? (static_cast<int64_t>(M) + 3) / 4 : M));
   const dim3 block(T == 32 ? 128 : T);
   const uint4* xv = static_cast<const uint4*>(x);
   const uint4* rv = static_cast<const uint4*>(residual);

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 import torch
@@ -109,8 +110,7 @@ def load():
     L.residual_rmsnorm_fp8.argtypes = [P, P, P, ctypes.c_float, I32, I32, P, P, P, P]
     L.lmhead_quantize_fp8.argtypes = [P, I32, I32, P, P, P]
     L.lmhead_logits_fp8.argtypes = [P, P, P, P, I32, I32, I32, P, I32, I64, P, SZ, P]
-    L.beam_attention.argtypes = [P, I64, P, P, I64, I64, I32, I32, P, I32, P, I32, P, P, P, I32,
-                                 I32, I32, I32, I32, ctypes.c_float, P, I64, P, SZ, P]
+    L.beam_attention.argtypes = [P, P]
     L.sidbeam_last_error.argtypes = []
     L.sidbeam_last_error.restype = ctypes.c_char_p
     L.sidbeam_version.argtypes = []
@@ -451,6 +451,10 @@ def lmhead_logits_fp8(hidden_q, hidden_scale, w_q, w_scale, out, workspace, stre
             dtype, ld, workspace.data_ptr(), workspace.nbytes)
 
 
+# The fields of sidbeam_attention in the header's order (native alignment).
+_ATTENTION = struct.Struct("PqPPqqiiPPPPPiiiiiiifPqPN").pack
+
+
 def beam_attention(q, k_cache, v_cache, cache_len, out, workspace, page_table=None, level=0,
                    k_beam=None, v_beam=None, bp_parent=None, scale=None, stream=None):
     """Attention of beam rows over their request's prompt cache and, for level > 0,
@@ -489,7 +493,7 @@ def beam_attention(q, k_cache, v_cache, cache_len, out, workspace, page_table=No
         token = Hkv * D
     if n_pages == 1:
         page = page_size * token
-    table, per, kb, vb, bp = None, 0, None, None, None
+    table = per = kb = vb = bp = 0
     if not (at >= 0 and q.dtype is _BF16 and k_cache.dtype is _BF16 and v_cache.dtype is _BF16
             and out.dtype is _BF16 and k_cache.get_device() == at and v_cache.get_device() == at
             and out.get_device() == at and workspace.get_device() == at
@@ -514,10 +518,11 @@ def beam_attention(q, k_cache, v_cache, cache_len, out, workspace, page_table=No
                     (k_beam, "k_beam", _BF16, (k_beam.shape[0], *beams)),
                     (v_beam, "v_beam", _BF16, (v_beam.shape[0], *beams)))
         bp, kb, vb = bp_parent.data_ptr(), k_beam.data_ptr(), v_beam.data_ptr()
-    _run_on(at, stream, (_lib or load()).beam_attention, q.data_ptr(), q_row, k_cache.data_ptr(),
-            v_cache.data_ptr(), page, token, n_pages, page_size, table, per, cache_len.data_ptr(),
-            level, bp, kb, vb, R, B, H, Hkv, D, D ** -0.5 if scale is None else scale,
-            out.data_ptr(), o_row, workspace.data_ptr(), workspace.nbytes)
+    _run_on(at, stream, (_lib or load()).beam_attention, _ATTENTION(
+        q.data_ptr(), q_row, k_cache.data_ptr(), v_cache.data_ptr(), page, token, n_pages,
+        page_size, table, cache_len.data_ptr(), bp, kb, vb, per, level, R, B, H, Hkv, D,
+        D ** -0.5 if scale is None else scale, out.data_ptr(), o_row, workspace.data_ptr(),
+        workspace.nbytes))
 
 
 def sidbeam_get_device_status(workspace, stream=None) -> int:
