@@ -242,9 +242,11 @@ __global__ void __launch_bounds__(kDual ? 640 : 512, 1)
     fence_mbar_init();
   }
   if (warp == 12) tmem_alloc(&bar.tmem, 512);
+  wait_prior();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  release_next();
   // All 512 columns are this CTA's, so they begin at column 0.
   constexpr uint32_t tmem = 0u;
   const int quarter = warp & 3;
@@ -1170,20 +1172,9 @@ int launch_kernel(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& m
       if (dev >= 0 && dev < 64) done[dev] = true;
     }
   }
-  cudaLaunchConfig_t lc{};
-  lc.gridDim = dim3(static_cast<unsigned>(kSplit ? a.units * a.split : std::min(a.units, sms)));
-  lc.blockDim = dim3(P::kThreads);
-  lc.dynamicSmemBytes = P::kSmem;
-  lc.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = a.split;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  lc.attrs = attr;
-  lc.numAttrs = kSplit ? 1 : 0;
-  e = cudaLaunchKernelEx(&lc, kernel, mk, mv, a);
-  if (e == cudaSuccess) e = cudaGetLastError();
+  const unsigned grid = static_cast<unsigned>(kSplit ? a.units * a.split : std::min(a.units, sms));
+  e = launch_dependent(kernel, dim3(grid), P::kThreads, P::kSmem, kSplit ? a.split : 1, stream, mk,
+                       mv, a);
   return e == cudaSuccess ? SIDBEAM_OK : cuda_error(e, "beam_attention: launch");
 }
 

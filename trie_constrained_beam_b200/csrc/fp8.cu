@@ -67,6 +67,8 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T)
                    float eps, int M, int d, uint4* residual_out, uint2* __restrict__ q,
                    float* __restrict__ scale) {
   constexpr int kRows = T == 32 ? 4 : 1;
+  wait_prior();
+  release_next();
   const int t = T == 32 ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + (T == 32 ? threadIdx.x >> 5 : 0);
   if (row >= M) return;
@@ -146,6 +148,8 @@ __global__ void __launch_bounds__(kQuantThreads)
     quantize_kernel(const uint4* __restrict__ w, int V, int d, uint2* __restrict__ q,
                     float* __restrict__ scale) {
   __shared__ float part[kQuantThreads / 32];
+  wait_prior();
+  release_next();
   const int nb = (d + kBlock - 1) / kBlock;
   const int bc = blockIdx.x, br = blockIdx.y;
   const int chunks = d >> 3;
@@ -189,23 +193,18 @@ __global__ void __launch_bounds__(kQuantThreads)
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 template <int T>
-void launch_rmsnorm(int k, const void* x, const void* residual, const void* weight, float eps,
-                    int M, int d, void* residual_out, void* q, float* scale, cudaStream_t s) {
+cudaError_t launch_rmsnorm(int k, const void* x, const void* residual, const void* weight,
+                           float eps, int M, int d, void* residual_out, void* q, float* scale,
+                           cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(T == 32 ? (static_cast<int64_t>(M) + 3) / 4 : M));
-  const dim3 block(T == 32 ? 128 : T);
-  const uint4* xv = static_cast<const uint4*>(x);
-  const uint4* rv = static_cast<const uint4*>(residual);
-  const uint4* wv = static_cast<const uint4*>(weight);
-  uint4* ov = static_cast<uint4*>(residual_out);
-  uint2* qv = static_cast<uint2*>(q);
-  if (k <= 1)
-    rmsnorm_kernel<T, 1><<<grid, block, 0, s>>>(xv, rv, wv, eps, M, d, ov, qv, scale);
-  else if (k <= 2)
-    rmsnorm_kernel<T, 2><<<grid, block, 0, s>>>(xv, rv, wv, eps, M, d, ov, qv, scale);
-  else if (k <= 4)
-    rmsnorm_kernel<T, 4><<<grid, block, 0, s>>>(xv, rv, wv, eps, M, d, ov, qv, scale);
-  else
-    rmsnorm_kernel<T, 8><<<grid, block, 0, s>>>(xv, rv, wv, eps, M, d, ov, qv, scale);
+  const auto kernel = k <= 1   ? rmsnorm_kernel<T, 1>
+                      : k <= 2 ? rmsnorm_kernel<T, 2>
+                      : k <= 4 ? rmsnorm_kernel<T, 4>
+                               : rmsnorm_kernel<T, 8>;
+  return launch_dependent(kernel, grid, T == 32 ? 128 : T, 0, 1, s, static_cast<const uint4*>(x),
+                          static_cast<const uint4*>(residual), static_cast<const uint4*>(weight),
+                          eps, M, d, static_cast<uint4*>(residual_out), static_cast<uint2*>(q),
+                          scale);
 }
 
 }  // namespace
@@ -230,16 +229,16 @@ extern "C" int residual_rmsnorm_fp8(const void* x, const void* residual, const v
     return set_error(SIDBEAM_ERR_ALIGNMENT, "residual_rmsnorm_fp8: pointers must be 16-byte aligned");
   const int chunks = d / 8;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
   if (chunks <= 64)
-    launch_rmsnorm<32>((chunks + 31) / 32, x, residual, weight, eps, M, d, residual_out, hidden_q,
+    e = launch_rmsnorm<32>((chunks + 31) / 32, x, residual, weight, eps, M, d, residual_out, hidden_q,
                        hidden_scale, s);
   else if (chunks <= 128 * 8)
-    launch_rmsnorm<128>((chunks + 127) / 128, x, residual, weight, eps, M, d, residual_out,
+    e = launch_rmsnorm<128>((chunks + 127) / 128, x, residual, weight, eps, M, d, residual_out,
                         hidden_q, hidden_scale, s);
   else
-    launch_rmsnorm<256>((chunks + 255) / 256, x, residual, weight, eps, M, d, residual_out,
+    e = launch_rmsnorm<256>((chunks + 255) / 256, x, residual, weight, eps, M, d, residual_out,
                         hidden_q, hidden_scale, s);
-  const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? SIDBEAM_OK : cuda_error(e, "residual_rmsnorm_fp8: launch");
 }
 
@@ -255,8 +254,8 @@ extern "C" int lmhead_quantize_fp8(const void* w_sid, int V, int d, void* w_q, f
     return set_error(SIDBEAM_ERR_ALIGNMENT, "lmhead_quantize_fp8: pointers must be 16-byte aligned");
   const dim3 grid(static_cast<unsigned>((d + kBlock - 1) / kBlock),
                   static_cast<unsigned>((V + kBlock - 1) / kBlock));
-  quantize_kernel<<<grid, kQuantThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+  const cudaError_t e = launch_dependent(
+      quantize_kernel, grid, kQuantThreads, 0, 1, static_cast<cudaStream_t>(stream),
       static_cast<const uint4*>(w_sid), V, d, static_cast<uint2*>(w_q), w_scale);
-  const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? SIDBEAM_OK : cuda_error(e, "lmhead_quantize_fp8: launch");
 }

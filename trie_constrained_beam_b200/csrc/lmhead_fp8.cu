@@ -102,9 +102,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 9) tmem_alloc(tmem_slot, 512);
+  wait_prior();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  release_next();
   constexpr uint32_t tmem = 0u;  // all 512 columns: they begin at column 0
 
   // Registers: 384 threads start with 168 each; 232 + 232 + 40 = 3 * 168.
@@ -322,9 +324,11 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(&tmem_slot, P::kTmemCols);
+  wait_prior();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  release_next();
   const uint32_t tmem = tmem_slot;
 
   float acc[NB];
@@ -488,8 +492,8 @@ int launch_gemm(const void* h, const void* w, const Fp8Args& a, int d, cudaStrea
   const int64_t tiles =
       static_cast<int64_t>((a.M + kTileM - 1) / kTileM) * ((a.V + kTileN - 1) / kTileN);
   const int grid = static_cast<int>(std::min<int64_t>(tiles, device_sm_count()));
-  fp8_gemm_kernel<kTileN, T><<<grid, kThreads, GemmPlan<kTileN>::kSmem, stream>>>(mh, mw, a);
-  e = cudaGetLastError();
+  e = launch_dependent(fp8_gemm_kernel<kTileN, T>, dim3(static_cast<unsigned>(grid)), kThreads,
+                       GemmPlan<kTileN>::kSmem, 1, stream, mh, mw, a);
   return e == cudaSuccess ? SIDBEAM_OK : cuda_error(e, "lmhead_logits_fp8: launch");
 }
 
@@ -515,20 +519,9 @@ int launch_rows(const void* h, const void* w, const Fp8Args& a, int d, cudaStrea
   static bool done[64] = {};
   cudaError_t e = opt_in(fp8_rows_kernel<NB, T>, 224 * 1024, done);
   if (e != cudaSuccess) return cuda_error(e, "lmhead_logits_fp8: cudaFuncSetAttribute");
-  cudaLaunchConfig_t lc{};
-  lc.gridDim = dim3(static_cast<unsigned>(tiles * split), static_cast<unsigned>(groups));
-  lc.blockDim = dim3(kRowThreads);
-  lc.dynamicSmemBytes = smem;
-  lc.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = split;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  lc.attrs = attr;
-  lc.numAttrs = 1;
-  e = cudaLaunchKernelEx(&lc, fp8_rows_kernel<NB, T>, mh, mw, a, split, stages);
-  if (e == cudaSuccess) e = cudaGetLastError();
+  e = launch_dependent(fp8_rows_kernel<NB, T>,
+                       dim3(static_cast<unsigned>(tiles * split), static_cast<unsigned>(groups)),
+                       kRowThreads, smem, split, stream, mh, mw, a, split, stages);
   return e == cudaSuccess ? SIDBEAM_OK : cuda_error(e, "lmhead_logits_fp8: launch");
 }
 

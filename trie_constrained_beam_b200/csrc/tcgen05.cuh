@@ -271,6 +271,22 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return r;
 }
 
+// ------------------------------------------------------------ dependent launches
+// These kernels are launched as programmatic dependents: their CTAs may start,
+// and set up what touches no global memory, while the kernel before them on the
+// stream still runs. Every thread calls wait_prior() before its first access to
+// global memory: it returns when that kernel has ended. release_next() lets the
+// next kernel's CTAs start in the same way, once every CTA has called it. It comes
+// after wait_prior(), so that at most one kernel waits on the device, and after
+// this CTA has its TMEM: a CTA of the next kernel on the same SM could otherwise
+// take the columns first and then wait for this one.
+__device__ __forceinline__ void wait_prior() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void release_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ------------------------------------------------------------ clusters
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -305,6 +321,28 @@ __device__ __forceinline__ float4 ld_peer4(uint32_t addr) {
 }
 
 }  // namespace dev
+
+// Launches a kernel that calls wait_prior(), in clusters of `cluster` CTAs.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, int smem, int cluster,
+                             cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t lc{};
+  lc.gridDim = grid;
+  lc.blockDim = dim3(static_cast<unsigned>(threads));
+  lc.dynamicSmemBytes = static_cast<size_t>(smem);
+  lc.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&lc, kernel, args...);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
 
 // cuTensorMapEncodeTiled of the loaded driver (null when there is none).
 inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
