@@ -168,6 +168,16 @@ def test_long_prompts_few_rows(tcb, R, B, S):
     assert torch.equal(first, c.out)   # joined in a fixed order
 
 
+@pytest.mark.parametrize("S", [256, 257, 384, 512, 900, 1024])
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 64)])
+def test_split_over_few_tiles(tcb, S, D, page):
+    """Two to eight key tiles over up to eight CTAs, some of which have none: the
+    requests' own lengths are shorter than the capacity that the split goes by."""
+    c = Case(4, 3, 2, 1, D, [S, 1, 130, 0], level=1, page=page, seed=S + D)
+    c.run(tcb)
+    c.check()
+
+
 @pytest.mark.parametrize("R,B,H,Hkv,D,level,page", [(250, 1, 4, 2, 128, 0, 16), (330, 2, 1, 1, 64, 1, 0),
                                                     (80, 66, 4, 2, 64, 2, 0), (76, 67, 4, 2, 128, 1, 64)])
 def test_many_units(tcb, R, B, H, Hkv, D, level, page):

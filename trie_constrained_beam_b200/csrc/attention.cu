@@ -64,11 +64,22 @@ constexpr float kNegInf = -INFINITY;
 //         each and share every key tile, which is loaded once for both.
 //  else:  a unit is one row tile; the streams take every other key tile, and the
 //         two (m, l, O) are joined at its end.
-// CTAs are persistent over units, with the rows' work in a warp group of its own:
+// CTAs are persistent over units, with a warp group per row tile for the rows' work:
 // while the streams run a unit, it scores the rows' ancestors and loads the next
 // unit's Q; while they run the next one, it joins, normalises and writes. Few
 // units are split over the keys among the CTAs of a cluster instead, and joined
 // through distributed shared memory in rank order.
+//
+// What bounds it, measured with 16 query and 8 key heads of 128:
+//  - Many rows, long prompts: the softmax, whose exponentials and conversions share
+//    their issue slots with the TMEM reads. 16 requests x 512 beams: 543 us over 8192
+//    tokens (1,013 TFLOP/s), 147 us over 2048, 82 us over 1024 (841), 26 us over 128.
+//  - Ancestors: 1024 tokens and 1, 2 or 4 levels take 100, 105 or 137 us against 82:
+//    each row gathers its own levels' keys and values, and the rows' warp groups
+//    take longer over them than the streams over the prompt.
+//  - One row a head (32 requests x 5000 tokens): the cache's bytes, 6.0 TB/s from
+//    pages of 64 (92% of the copy bandwidth).
+//  - One request, one row: latency. 128 tokens take 6.5 us, 1000 tokens 9.1.
 constexpr int kRows = 128;
 constexpr int kKeys = 128;
 constexpr int kMaxSplitLog2 = 3;
@@ -1194,11 +1205,24 @@ int launch_attention(AttnArgs& a, cudaStream_t stream) {
   a.units = static_cast<int>(units);
   const int64_t cap = a.table ? static_cast<int64_t>(a.table_stride) * a.page_size : a.page_size;
   const int64_t max_tiles = (cap + kKeys - 1) / kKeys;
-  // CTAs per unit: while they fit the SMs and each has two key tiles.
+  // CTAs per unit: doubled while all clusters run at once and each CTA has a key tile.
+  // One row, 16 / 8 heads of 128, us on 1, 2, 4, 8 CTAs a unit:
+  //   384 tokens    9.4   9.5   8.5   8.9        1024   15.2  12.9   9.7   9.1
+  //   512          10.2   9.6   8.6   9.1        2048   25.4  18.3  13.1  10.3
+  // (256 tokens: 7.3, split 8.4.) Two rows of 2048: 25.4, 18.3, 13.4, and 19.8 on 8,
+  // since 16 clusters of 8 do not run at once.
   a.split_log2 = 0;
-  while (a.split_log2 < kMaxSplitLog2 && (units << (a.split_log2 + 1)) <= sms &&
-         (4 << a.split_log2) <= max_tiles)
+  while (a.split_log2 < kMaxSplitLog2 && max_tiles > 2 && (2 << a.split_log2) <= max_tiles + 1 &&
+         units << (a.split_log2 + 1) <= sms) {
+    static std::mutex mu;
+    static int cache[64][4] = {};
+    int room = 0;
+    const cudaError_t e = clusters_at_once(attention_kernel<D, kDual, true, true>, P::kThreads,
+                                           P::kSmem, a.split_log2 + 1, mu, cache, &room);
+    if (e != cudaSuccess) return cuda_error(e, "beam_attention: cudaOccupancyMaxActiveClusters");
+    if (units > room) break;
     ++a.split_log2;
+  }
   a.split = 1 << a.split_log2;
   if (a.level > 0)
     return a.split > 1 ? launch_kernel<D, kDual, true, true>(a, mk, mv, sms, stream)
@@ -1307,8 +1331,11 @@ extern "C" int beam_attention(const sidbeam_attention* args, void* stream) {
   a.out_stride = out_row_stride;
   a.status = static_cast<uint32_t*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // Two row tiles a unit where there are two; long paths need the table space
-  // that one tile leaves.
+  // Two row tiles a unit where there are two: each key tile is read, and each page
+  // of it asked for, once for 256 rows, and two warp groups see to the ancestors. For
+  // 16 x 512 beams, 1024 tokens (one tile a unit in brackets): 82 us (81), at 4 levels
+  // 137 (206), from pages of 16 88 (135); over 128 tokens 26 (31), over 8192 543 (519).
+  // More than 8 levels need the table space that one tile leaves.
   const bool dual = static_cast<int64_t>(B) * a.G > kRows && level <= 8;
   if (D == 64)
     return dual ? launch_attention<64, true>(a, s) : launch_attention<64, false>(a, s);

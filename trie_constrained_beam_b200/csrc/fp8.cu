@@ -58,12 +58,19 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
 // T threads own a row, each K chunks of 8 consecutive elements, chunk i + k * T
 // (16-byte loads; 16 neighbouring threads hold one scale block). The row stays
 // in registers between its sum of squares and its quantisation, so it is read
-// once: 7 bytes per element in all, the bound of this kernel. T = 32 (four rows
-// per CTA, warp shuffles only) keeps up to 16 loads per lane in flight; larger
-// rows, and few rows, are spread over a CTA of 256 threads.
+// once: 7 bytes per element in all, the bound of this kernel (8192 rows of 2048:
+// 20.4 us, 89% of the copy bandwidth). T threads a row by its size (us per call at
+// 8192 or 16384 rows, T = 32 four rows to a CTA):
+//   d      256    512    1024   2048
+//   32     8.3   14.3    23.8   27.2
+//   128   17.0   20.5    24.6   22.6   (256 threads at 2048: 24.7)
+// up to 512 a warp wins, its shuffles being the whole sum; at 1024 the two are
+// level with many rows and 128 threads win with few (512 rows: 4.2 against 5.2);
+// above, a warp's registers hold too few rows in flight. 256 threads only where
+// 128 would need more than 8 chunks each.
 template <int T, int K>
 __global__ void __launch_bounds__(T == 32 ? 128 : T)
-    rmsnorm_kernel(const uint4* x, const uint4* residual, const uint4* __restrict__ weight,
+    rmsnorm_kernel(const uint4* x, const uint4* residual, const uint4* weight,
                    float eps, int M, int d, uint4* residual_out, uint2* __restrict__ q,
                    float* __restrict__ scale) {
   constexpr int kRows = T == 32 ? 4 : 1;
@@ -102,6 +109,13 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T)
           make_uint4(bf16x2(h[k][0], h[k][1]), bf16x2(h[k][2], h[k][3]),
                      bf16x2(h[k][4], h[k][5]), bf16x2(h[k][6], h[k][7]));
   }
+  // The weight, on its way during the sum. (No read-only loads here: they are not
+  // ordered behind wait_prior().)
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    a[k] = make_uint4(0u, 0u, 0u, 0u);
+    if (t + k * T < chunks) a[k] = weight[t + k * T];
+  }
   sum = warp_sum(sum);
   if constexpr (T > 32) {
     __shared__ float part[T / 32];
@@ -117,8 +131,8 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T)
   for (int k = 0; k < K; ++k) {
     const int c = t + k * T;
     const bool in = c < chunks;
-    float w[8] = {};
-    if (in) unpack8(weight[c], w);
+    float w[8];
+    unpack8(a[k], w);
     float amax = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -141,11 +155,13 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T)
 // ------------------------------------------------------------ weight quantisation
 // One CTA per block of 128 codes x 128 columns, kept in registers between its
 // maximum and its rounding: 16 threads per row, 16 rows per pass, 8 passes.
-// Bound by the 3 bytes per element it moves.
+// Bound by the 3 bytes per element it moves (8192 x 2048: 11.4 us, 68% of the copy
+// bandwidth: each CTA reads once and writes once, and 1024 of them are one wave
+// whose start and end count); a small weight (500 x 1040) by its 2 us of latency.
 constexpr int kQuantThreads = 256;
 
 __global__ void __launch_bounds__(kQuantThreads)
-    quantize_kernel(const uint4* __restrict__ w, int V, int d, uint2* __restrict__ q,
+    quantize_kernel(const uint4* w, int V, int d, uint2* __restrict__ q,
                     float* __restrict__ scale) {
   __shared__ float part[kQuantThreads / 32];
   wait_prior();
@@ -231,8 +247,8 @@ extern "C" int residual_rmsnorm_fp8(const void* x, const void* residual, const v
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (chunks <= 64)
-    e = launch_rmsnorm<32>((chunks + 31) / 32, x, residual, weight, eps, M, d, residual_out, hidden_q,
-                       hidden_scale, s);
+    e = launch_rmsnorm<32>((chunks + 31) / 32, x, residual, weight, eps, M, d, residual_out,
+                           hidden_q, hidden_scale, s);
   else if (chunks <= 128 * 8)
     e = launch_rmsnorm<128>((chunks + 127) / 128, x, residual, weight, eps, M, d, residual_out,
                         hidden_q, hidden_scale, s);

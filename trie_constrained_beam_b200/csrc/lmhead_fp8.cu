@@ -48,6 +48,12 @@ struct Fp8Args {
 // (warp 8: TMA, warp 9: MMA). A block's MMAs take 512 cycles, and so at least does
 // its way out: 128 KB of TMEM reads and 32K FMAs per SM; the epilogue keeps three
 // loads of 32 columns in turn, so that neither waits for the other.
+//
+// 4096 x 8192 x 2048 to fp32: 82 us, 1,676 TFLOP/s, half of the 8-bit rate. What
+// bounds it is the way in: a block takes about 1,130 cycles, in which every SM
+// reads 48 KB, 12 TB/s out of L2 in all; then a tile's store, about 6,700 cycles
+// that overlap the next tile's first blocks only. Four more epilogue warps a group
+// (64 columns each) measured 88 us against 83.
 constexpr int kTileM = 128;
 constexpr int kABytes = kTileM * kBlock;
 constexpr int kThreads = 384;
@@ -281,6 +287,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // which is all that counts here, is read once. The CTAs of a cluster share a
 // tile and split d; each adds up its part in registers, and the parts meet
 // through distributed shared memory in rank order (the same sum every time).
+//
+// Bound by the weight's bytes and the start and end of a call: 32 rows of
+// 8192 x 2048 take 7.5 us, a third of the copy bandwidth (2.7 us of bytes, about
+// 2 us for an empty kernel, then the first loads' and the cluster's latency).
 constexpr int kRowThreads = 192;  // TMA warp, MMA warp, 4 epilogue warps
 
 template <int NB>
@@ -506,12 +516,26 @@ int launch_rows(const void* h, const void* w, const Fp8Args& a, int d, cudaStrea
   const int tiles = (a.V + kTileM - 1) / kTileM;
   const int groups = (a.M + NB - 1) / NB;
   const int sms = device_sm_count();
-  // CTAs per tile: up to 8 while the grid fits the SMs and every CTA has a block.
-  int split = 1;
-  while (split < 8 && split * 2 <= a.nb && tiles * groups * split * 2 <= sms) split *= 2;
+  // CTAs per tile: up to 8 while all clusters run at once, one CTA to an SM, and
+  // every CTA has a block (1 x 8192 x 2048: 6.2 us, unsplit 8.7; 16 x 4096 x 8192:
+  // 11.8, unsplit 28.6; for 16 tiles, 8 CTAs each instead of 4 would not run at once:
+  // 32 x 2048 x 2048 6.2 instead of 5.7).
+  int log2 = 0;
+  while (log2 < 3 && (2 << log2) <= a.nb && tiles * groups << (log2 + 1) <= sms) {
+    static std::mutex mu;
+    static int cache[64][4] = {};
+    int fit = 0;
+    const cudaError_t e =
+        clusters_at_once(fp8_rows_kernel<NB, T>, kRowThreads, 224 * 1024, log2 + 1, mu, cache, &fit);
+    if (e != cudaSuccess)
+      return cuda_error(e, "lmhead_logits_fp8: cudaOccupancyMaxActiveClusters");
+    if (tiles * groups > fit) break;
+    ++log2;
+  }
+  const int split = 1 << log2;
   const int n = (a.nb + split - 1) / split;
   const int table = n * NB * 4;
-  // More CTAs than SMs: two to an SM.
+  // More CTAs than SMs: two to an SM (32 x 32768 x 2048: 16.7 us, one to an SM 22.8).
   const int room = tiles * groups * split > sms ? 112 : 224;
   const int budget = room * 1024 - 1024 - table;
   const int stages = std::max(2, std::min({8, n, budget / P::kStage}));
@@ -525,6 +549,11 @@ int launch_rows(const void* h, const void* w, const Fp8Args& a, int d, cudaStrea
   return e == cudaSuccess ? SIDBEAM_OK : cuda_error(e, "lmhead_logits_fp8: launch");
 }
 
+// Few rows up to 32: with 64 rows of 8192 x 2048 the few-rows kernel took 9.8 us, the
+// other 8.1. 16 or 32 of them a tile, since a tile's promotion costs its whole width.
+// Above, 128 codes a tile while 256 would leave half of the SMs without one:
+// 129 rows (64 wide tiles) 9.3 us against 13.4, 512 rows (128 wide tiles) 17.0
+// against 15.0.
 template <typename T>
 int launch(const void* h, const void* w, const Fp8Args& a, int d, cudaStream_t stream) {
   if (a.M <= 16) return launch_rows<16, T>(h, w, a, d, stream);

@@ -344,6 +344,42 @@ cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, int s
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
+// Clusters of 2^log2 CTAs of `kernel` that run at once on the current device, one CTA
+// to an SM. A cluster lies within one GPC, so this is less than SMs / 2^log2 (16
+// clusters of 8 do not fit 148 SMs: the last ones wait for a whole round). Asked
+// once per device and size; `cache` is the kernel's own, zero at first.
+template <typename K>
+cudaError_t clusters_at_once(K kernel, int threads, int smem, int log2, std::mutex& mu,
+                             int (&cache)[64][4], int* out) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  int fresh = 0;
+  int& n = dev < 64 ? cache[dev][log2] : fresh;
+  if (n == 0) {
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = dim3(1u << log2);
+    lc.blockDim = dim3(static_cast<unsigned>(threads));
+    lc.dynamicSmemBytes = static_cast<size_t>(smem);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1u << log2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, kernel, &lc);
+    if (e != cudaSuccess) {
+      n = 0;
+      return e;
+    }
+  }
+  *out = n;
+  return cudaSuccess;
+}
+
 // cuTensorMapEncodeTiled of the loaded driver (null when there is none).
 inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static std::once_flag once;
