@@ -49,11 +49,12 @@ struct Fp8Args {
 // its way out: 128 KB of TMEM reads and 32K FMAs per SM; the epilogue keeps three
 // loads of 32 columns in turn, so that neither waits for the other.
 //
-// 4096 x 8192 x 2048 to fp32: 82 us, 1,676 TFLOP/s, half of the 8-bit rate. What
-// bounds it is the way in: a block takes about 1,130 cycles, in which every SM
-// reads 48 KB, 12 TB/s out of L2 in all; then a tile's store, about 6,700 cycles
-// that overlap the next tile's first blocks only. Four more epilogue warps a group
-// (64 columns each) measured 88 us against 83.
+// 4096 x 8192 x 2048 to fp32: 82-87 us, 1,600-1,680 TFLOP/s, half of the 8-bit rate.
+// A block takes about 1,130 cycles, and a tile's store about 6,700 that overlap the
+// next tile's first blocks only. No unit is full: the tensor pipe 41%, issue slots
+// 48%, L2 26%, DRAM 18% of its rate; each SM takes in 48 KB a block, 43 bytes a
+// cycle (12 TB/s over all SMs). Twice the epilogue warps with half the columns each
+// measured 88 us against 83, so it is not their latency alone.
 constexpr int kTileM = 128;
 constexpr int kABytes = kTileM * kBlock;
 constexpr int kThreads = 384;
@@ -537,8 +538,8 @@ int launch_rows(const void* h, const void* w, const Fp8Args& a, int d, cudaStrea
   const int table = n * NB * 4;
   // More CTAs than SMs: two to an SM (32 x 32768 x 2048: 16.7 us, one to an SM 22.8).
   const int room = tiles * groups * split > sms ? 112 : 224;
-  const int budget = room * 1024 - 1024 - table;
-  const int stages = std::max(2, std::min({8, n, budget / P::kStage}));
+  const int left = room * 1024 - 1024 - table;
+  const int stages = std::max(2, std::min({8, n, left / P::kStage}));
   const int smem = 1024 + std::max(stages * P::kStage + table, NB * 128 * 4);
   static bool done[64] = {};
   cudaError_t e = opt_in(fp8_rows_kernel<NB, T>, 224 * 1024, done);
