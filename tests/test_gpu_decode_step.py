@@ -129,3 +129,29 @@ def _search(tcb, dtype, captured):
 def test_decode_loop(tcb, dtype, captured):
     import torch
     _search(tcb, torch.bfloat16 if dtype == "bf16" else torch.float32, captured)
+
+
+def test_step_hidden_status_reaches_the_search(tcb, monkeypatch):
+    """A wait that gives up inside the 8-bit product (its bit set here behind the
+    product, in the word that the product was handed) is what the search's status
+    reads; the next step starts clean."""
+    import torch
+    from trie_constrained_beam_b200 import native
+    R, n, depth, V, d = 2, 8, 2, 200, 256
+    trie = tcb.sid_trie_build(host.draw_catalog(7, 1000, [V] * depth), [V] * depth)
+    search = tcb.BeamSearch(trie, R, n, V, depth=depth)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    w = torch.randn((V, d), device="cuda", generator=g).to(torch.bfloat16)
+    head = tcb.LmheadFp8(w, torch.ones(d, dtype=torch.bfloat16, device="cuda"), R * n)
+    x = torch.randn((R, d), device="cuda", generator=g).to(torch.bfloat16)
+    search.step_hidden(0, head, x)
+    assert tcb.sidbeam_get_device_status(search.workspace) == 0
+    product = native.lmhead_logits_fp8
+
+    def gives_up(hq, hs, wq, ws, out, workspace, stream=None):
+        product(hq, hs, wq, ws, out, workspace, stream=stream)
+        workspace[:1].bitwise_or_(2)
+    monkeypatch.setattr(native, "lmhead_logits_fp8", gives_up)
+    search.step_hidden(0, head, x)
+    assert tcb.sidbeam_get_device_status(search.workspace) == tcb.native.SIDBEAM_ERR_TIMEOUT
+    assert tcb.sidbeam_get_device_status(search.workspace) == 0

@@ -1,0 +1,61 @@
+"""CPU checks of the buffers and the plumbing of search.py: the library's entry
+points are replaced by recorders, so no device is needed."""
+import pytest
+import torch
+
+import trie_constrained_beam_b200 as tcb
+from trie_constrained_beam_b200 import build, native
+
+TIMEOUT_BIT = 2  # of the status word, the first 4 bytes of a workspace
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """Every entry point that search.py calls, recorded; the 8-bit product gives up
+    on a wait, as the kernel reports it, in the workspace that it was handed."""
+    build.build()
+    seen = []
+
+    def product(hidden_q, hidden_scale, w_q, w_scale, out, workspace, stream=None):
+        seen.append(("lmhead_logits_fp8", workspace))
+        workspace[0] |= TIMEOUT_BIT
+
+    def record(name):
+        return lambda *args, **kw: seen.append((name, args, kw))
+    monkeypatch.setattr(native, "lmhead_logits_fp8", product)
+    for name in ("lmhead_quantize_fp8", "residual_rmsnorm_fp8", "beam_step", "beam_step_gumbel"):
+        monkeypatch.setattr(native, name, record(name))
+    return seen
+
+
+def _search(R=2, n=4, V=200, depth=2, **kw):
+    return tcb.BeamSearch(None, R, n, V, depth=depth, device="cpu", **kw)
+
+
+def _head(V=200, d=256, max_rows=8, **kw):
+    return tcb.LmheadFp8(torch.zeros((V, d), dtype=torch.bfloat16),
+                         torch.ones(d, dtype=torch.bfloat16), max_rows, **kw)
+
+
+def _rows(m, d=256):
+    return torch.zeros((m, d), dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("temperature", [0.0, 0.7])
+def test_step_hidden_reports_in_the_searchs_status_word(calls, temperature):
+    """A product that gave up leaves logits of an earlier call: the status word that
+    a user of the search reads has to say so."""
+    search, head = _search(temperature=temperature), _head()
+    search.step_hidden(0, head, _rows(2))
+    assert int(search.workspace[0]) == TIMEOUT_BIT
+    assert [c[0] for c in calls][-1] == ("beam_step_gumbel" if temperature else "beam_step")
+
+
+def test_logits_alone_report_in_the_heads_status_word(calls):
+    head = _head()
+    head.logits(_rows(3))
+    assert int(head.workspace[0]) == TIMEOUT_BIT
+    own = torch.zeros(256, dtype=torch.uint8)
+    head.workspace.zero_()
+    head.logits(_rows(3), workspace=own)
+    assert int(own[0]) == TIMEOUT_BIT and int(head.workspace[0]) == 0

@@ -17,7 +17,8 @@ class LmheadFp8:
     once (``lmhead_quantize_fp8``) and the row buffers of up to ``max_rows`` rows.
 
     w_sid bf16 [V, d], norm_weight bf16 [d]; logits in ``dtype`` (bf16 or f32).
-    The buffers are rewritten by every call: one stream at a time.
+    The buffers are rewritten by every call: one stream at a time. ``workspace``
+    holds the status word of calls that are given no other.
     """
 
     def __init__(self, w_sid, norm_weight, max_rows: int, eps: float = 1e-6,
@@ -36,9 +37,10 @@ class LmheadFp8:
         self._logits = torch.empty((max_rows, -(-V // 8) * 8), dtype=dtype, device=dev)
         self.workspace = torch.zeros(256, dtype=torch.uint8, device=dev)
 
-    def logits(self, x, residual=None, residual_out=None, stream=None):
+    def logits(self, x, residual=None, residual_out=None, stream=None, workspace=None):
         """Logits [rows, V] of rows x (+ residual), bf16 [rows, d]; a view of this
-        object's buffer."""
+        object's buffer. ``workspace``: where the product reports a wait that gave
+        up (the logits then hold an earlier call's), default this object's."""
         rows = x.shape[0]
         if rows > self.max_rows:
             raise ValueError(f"{rows} rows, room for {self.max_rows}")
@@ -46,7 +48,8 @@ class LmheadFp8:
         native.residual_rmsnorm_fp8(x, residual, self.norm_weight, self.eps, residual_out, hq, hs,
                                     stream=stream)
         out = self._logits[:rows, :self.V]
-        native.lmhead_logits_fp8(hq, hs, self.w_q, self.w_scale, out, self.workspace,
+        native.lmhead_logits_fp8(hq, hs, self.w_q, self.w_scale, out,
+                                 self.workspace if workspace is None else workspace,
                                  stream=stream)
         return out
 
@@ -125,8 +128,10 @@ class BeamSearch:
     def step_hidden(self, t: int, head: LmheadFp8, x, residual=None, residual_out=None,
                     stream=None):
         """Step t from hidden states bf16 [rows(t), d]: residual RMS norm and
-        lm_head in 8 bits (``head``), then the constrained step on its logits."""
-        self.step(t, head.logits(x, residual, residual_out, stream=stream), stream=stream)
+        lm_head in 8 bits (``head``), then the constrained step on its logits. All
+        of them report in this search's workspace (``sidbeam_get_device_status``)."""
+        logits = head.logits(x, residual, residual_out, stream=stream, workspace=self.workspace)
+        self.step(t, logits, stream=stream)
 
     def skipped_rows(self, stream=None) -> int:
         """Rows left unread by row skipping since the last call."""
