@@ -59,3 +59,23 @@ def test_logits_alone_report_in_the_heads_status_word(calls):
     head.workspace.zero_()
     head.logits(_rows(3), workspace=own)
     assert int(own[0]) == TIMEOUT_BIT and int(head.workspace[0]) == 0
+
+
+def test_step_hidden_refuses_what_the_step_would_read_past(calls):
+    """beam_step reads rows(t) rows of V[t] logits: fewer rows than that, or a head
+    of fewer codes, would leave it with rows and columns that nothing has written
+    (past the buffer's end, where max_rows is smaller too)."""
+    search, head = _search(R=2, n=4, V=[200, 204]), _head(V=200, max_rows=8)
+    done = len(calls)
+    with pytest.raises(ValueError, match="rows"):
+        search.step_hidden(0, head, _rows(1))
+    with pytest.raises(ValueError, match="rows"):
+        search.step_hidden(1, _head(V=204, max_rows=2), _rows(2))
+    with pytest.raises(ValueError, match="codes"):
+        search.step_hidden(1, head, _rows(8))
+    assert all(c[0] == "lmhead_quantize_fp8" for c in calls[done:])   # nothing was launched
+    # A padded batch and a head of more codes are fine: the step reads the first of them.
+    search.step_hidden(0, head, _rows(5))
+    search.step_hidden(1, _head(V=300), _rows(8))
+    logits = calls[-1][1][2]
+    assert logits.shape == (8, 300) and logits.stride() == (304, 1)

@@ -129,7 +129,11 @@ class BeamSearch:
                     stream=None):
         """Step t from hidden states bf16 [rows(t), d]: residual RMS norm and
         lm_head in 8 bits (``head``), then the constrained step on its logits. All
-        of them report in this search's workspace (``sidbeam_get_device_status``)."""
+        of them report in this search's workspace (``sidbeam_get_device_status``).
+        Of more rows, or of a head with more codes, the step uses the first."""
+        if x.shape[0] < self.rows(t) or head.V < self.V[t]:
+            raise ValueError(f"step {t} takes {self.rows(t)} rows and {self.V[t]} codes, got "
+                             f"{x.shape[0]} rows and a head of {head.V} codes")
         logits = head.logits(x, residual, residual_out, stream=stream, workspace=self.workspace)
         self.step(t, logits, stream=stream)
 
