@@ -195,3 +195,29 @@ def test_python_checks_come_before_the_library():
     rows = torch.zeros((3, 1, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="rows"):
         tcb.beam_attention(rows, cache, cache, n, rows, torch.zeros(256, dtype=torch.uint8))
+
+
+def test_import_without_torchs_cuda_bindings():
+    """A torch built without CUDA has none of torch._C's CUDA functions: the package
+    imports and answers host calls, and refuses CPU tensors as elsewhere."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+import torch
+for name in [n for n in dir(torch._C) if n.startswith("_cuda_")]:
+    delattr(torch._C, name)
+import trie_constrained_beam_b200 as tcb
+assert tcb.beam_step_workspace_size(2, 4, 4, 100) > 0
+x = torch.zeros((2, 256), dtype=torch.bfloat16)
+try:
+    tcb.lmhead_quantize_fp8(x, x.to(torch.float8_e4m3fn), torch.zeros((1, 2)))
+except ValueError as e:
+    assert "CUDA" in str(e)
+else:
+    raise SystemExit("a CPU tensor was taken")
+print("imported")
+"""
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert done.returncode == 0 and "imported" in done.stdout, done.stderr

@@ -344,9 +344,6 @@ def fused_lmhead_step(trie, step, hidden, w_sid, parent_scores, parent_nodes, R,
     _check(rc)
 
 
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-
-
 def _refuse(index, *args):
     """Raises for the first argument (tensor, name, dtype, shape of a contiguous
     tensor or None) that does not fit a call on CUDA device `index`."""
@@ -374,9 +371,11 @@ def _fits(t, dtype, index, shape):
 
 def _run_on(index, stream, fn, *args):
     """Calls a C entry on CUDA device `index`: on `stream`, or on that device's
-    current stream."""
-    s = _raw_stream(index) if stream is None else stream.cuda_stream
-    if index == _current_device():
+    current stream. (torch._C's calls, without the wrappers of torch.cuda, are on
+    the way of every launch. A torch built without CUDA lacks them: they are looked
+    up here, not on import.)"""
+    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if index == torch._C._cuda_getDevice():
         rc = fn(*args, s)
     else:
         with torch.cuda.device(index):
