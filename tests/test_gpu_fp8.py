@@ -274,3 +274,29 @@ def test_argument_checks(tcb):
         tcb.residual_rmsnorm_fp8(x.cpu(), None, x[0], 1e-6, None, q, s)
     with pytest.raises(tcb.SidbeamError):
         tcb.residual_rmsnorm_fp8(x, None, x[0], -1.0, None, q, s)
+
+
+def test_head_made_on_a_side_stream(tcb):
+    """A head made on a side stream while the current one is busy: weight, scales and
+    status word are that stream's, none of them behind the current stream's work."""
+    import torch
+    V, d = 700, 512
+    rng = np.random.default_rng(12)
+    w = _bf16(0.02 * rng.standard_normal((V, d))).cuda()
+    g = _bf16(1 + 0.1 * rng.standard_normal(d)).cuda()
+    x = _bf16(rng.standard_normal((5, d))).cuda()
+    want = tcb.LmheadFp8(w, g, 5)
+    ref = want.logits(x).clone()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    busy = torch.randn((4096, 4096), device="cuda")
+    junk = torch.full((64, 256), 255, dtype=torch.uint8, device="cuda")
+    del junk                                  # freed, on the current stream
+    for _ in range(20):
+        busy = busy @ busy * 1e-4
+    head = tcb.LmheadFp8(w, g, 5, stream=side)
+    out = head.logits(x, stream=side)
+    side.synchronize()
+    assert tcb.sidbeam_get_device_status(head.workspace, stream=side) == 0
+    assert np.array_equal(_codes(head.w_q), _codes(want.w_q))
+    assert torch.equal(head.w_scale, want.w_scale) and torch.equal(out, ref)

@@ -79,3 +79,29 @@ def test_step_hidden_refuses_what_the_step_would_read_past(calls):
     search.step_hidden(1, _head(V=300), _rows(8))
     logits = calls[-1][1][2]
     assert logits.shape == (8, 300) and logits.stride() == (304, 1)
+
+
+def test_head_allocates_on_the_stream_it_quantises_on(calls, monkeypatch):
+    """Buffers made on the current stream and written by another one could be memory
+    that work queued on the current stream still uses, and a status word that is not
+    cleared yet: with a stream given, all of a head's buffers are that stream's."""
+    import contextlib
+    entered, made = [], []
+
+    @contextlib.contextmanager
+    def on(stream):
+        entered.append(stream)
+        yield
+        entered.pop()
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    for name in ("empty", "zeros"):
+        make = getattr(torch, name)
+        monkeypatch.setattr(torch, name, lambda *a, _make=make, **kw: (
+            made.append(entered[-1] if entered else None), _make(*a, **kw))[1])
+    w, norm = torch.ones((200, 256), dtype=torch.bfloat16), torch.ones(256, dtype=torch.bfloat16)
+    tcb.LmheadFp8(w, norm, 8, stream="side")
+    assert len(made) == 6 and set(made) == {"side"}
+    assert calls[-1][0] == "lmhead_quantize_fp8" and calls[-1][2]["stream"] == "side"
+    made.clear()
+    tcb.LmheadFp8(w, norm, 8)
+    assert set(made) == {None}

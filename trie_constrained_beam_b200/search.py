@@ -17,8 +17,9 @@ class LmheadFp8:
     once (``lmhead_quantize_fp8``) and the row buffers of up to ``max_rows`` rows.
 
     w_sid bf16 [V, d], norm_weight bf16 [d]; logits in ``dtype`` (bf16 or f32).
-    The buffers are rewritten by every call: one stream at a time. ``workspace``
-    holds the status word of calls that are given no other.
+    ``stream`` (default: the current one) quantises the weight and owns the
+    buffers, which every call rewrites: one stream at a time, in the caller's order.
+    ``workspace`` holds the status word of calls that are given no other.
     """
 
     def __init__(self, w_sid, norm_weight, max_rows: int, eps: float = 1e-6,
@@ -28,14 +29,19 @@ class LmheadFp8:
         nb = -(-d // native.FP8_BLOCK)
         self.V, self.d, self.eps, self.max_rows = V, d, float(eps), int(max_rows)
         self.norm_weight = norm_weight
-        self.w_q = torch.empty((V, d), dtype=torch.float8_e4m3fn, device=dev)
-        self.w_scale = torch.empty((-(-V // native.FP8_BLOCK), nb), dtype=torch.float32, device=dev)
+        # On `stream` as the quantisation is: memory that the current stream has freed
+        # may still be in use there, and the status word has to be zero before its
+        # first call.
+        with torch.cuda.stream(stream):
+            self.w_q = torch.empty((V, d), dtype=torch.float8_e4m3fn, device=dev)
+            self.w_scale = torch.empty((-(-V // native.FP8_BLOCK), nb), dtype=torch.float32,
+                                       device=dev)
+            self.hidden_q = torch.empty((max_rows, d), dtype=torch.float8_e4m3fn, device=dev)
+            self.hidden_scale = torch.empty((max_rows, nb), dtype=torch.float32, device=dev)
+            # Rows of whole 16-byte units, as beam_step reads them.
+            self._logits = torch.empty((max_rows, -(-V // 8) * 8), dtype=dtype, device=dev)
+            self.workspace = torch.zeros(256, dtype=torch.uint8, device=dev)
         native.lmhead_quantize_fp8(w_sid, self.w_q, self.w_scale, stream=stream)
-        self.hidden_q = torch.empty((max_rows, d), dtype=torch.float8_e4m3fn, device=dev)
-        self.hidden_scale = torch.empty((max_rows, nb), dtype=torch.float32, device=dev)
-        # Rows of whole 16-byte units, as beam_step reads them.
-        self._logits = torch.empty((max_rows, -(-V // 8) * 8), dtype=dtype, device=dev)
-        self.workspace = torch.zeros(256, dtype=torch.uint8, device=dev)
 
     def logits(self, x, residual=None, residual_out=None, stream=None, workspace=None):
         """Logits [rows, V] of rows x (+ residual), bf16 [rows, d]; a view of this
