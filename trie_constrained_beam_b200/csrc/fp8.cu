@@ -208,19 +208,15 @@ __global__ void __launch_bounds__(kQuantThreads)
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-template <int T>
-cudaError_t launch_rmsnorm(int k, const void* x, const void* residual, const void* weight,
-                           float eps, int M, int d, void* residual_out, void* q, float* scale,
+template <int T, int K>
+cudaError_t launch_rmsnorm(const void* x, const void* residual, const void* weight, float eps,
+                           int M, int d, void* residual_out, void* q, float* scale,
                            cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(T == 32 ? (static_cast<int64_t>(M) + 3) / 4 : M));
-  const auto kernel = k <= 1   ? rmsnorm_kernel<T, 1>
-                      : k <= 2 ? rmsnorm_kernel<T, 2>
-                      : k <= 4 ? rmsnorm_kernel<T, 4>
-                               : rmsnorm_kernel<T, 8>;
-  return launch_dependent(kernel, grid, T == 32 ? 128 : T, 0, 1, s, static_cast<const uint4*>(x),
-                          static_cast<const uint4*>(residual), static_cast<const uint4*>(weight),
-                          eps, M, d, static_cast<uint4*>(residual_out), static_cast<uint2*>(q),
-                          scale);
+  return launch_dependent(rmsnorm_kernel<T, K>, grid, T == 32 ? 128 : T, 0, 1, s,
+                          static_cast<const uint4*>(x), static_cast<const uint4*>(residual),
+                          static_cast<const uint4*>(weight), eps, M, d,
+                          static_cast<uint4*>(residual_out), static_cast<uint2*>(q), scale);
 }
 
 }  // namespace
@@ -243,18 +239,16 @@ extern "C" int residual_rmsnorm_fp8(const void* x, const void* residual, const v
   if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(residual_out) ||
       !aligned16(hidden_q) || (reinterpret_cast<uintptr_t>(hidden_scale) & 3u) != 0)
     return set_error(SIDBEAM_ERR_ALIGNMENT, "residual_rmsnorm_fp8: pointers must be 16-byte aligned");
-  const int chunks = d / 8;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (chunks <= 64)
-    e = launch_rmsnorm<32>((chunks + 31) / 32, x, residual, weight, eps, M, d, residual_out,
-                           hidden_q, hidden_scale, s);
-  else if (chunks <= 128 * 8)
-    e = launch_rmsnorm<128>((chunks + 127) / 128, x, residual, weight, eps, M, d, residual_out,
-                        hidden_q, hidden_scale, s);
-  else
-    e = launch_rmsnorm<256>((chunks + 255) / 256, x, residual, weight, eps, M, d, residual_out,
-                        hidden_q, hidden_scale, s);
+  const int chunks = d / 8;  // T * K of them at most
+  const auto launch = chunks <= 32        ? launch_rmsnorm<32, 1>
+                      : chunks <= 64      ? launch_rmsnorm<32, 2>
+                      : chunks <= 128     ? launch_rmsnorm<128, 1>
+                      : chunks <= 128 * 2 ? launch_rmsnorm<128, 2>
+                      : chunks <= 128 * 4 ? launch_rmsnorm<128, 4>
+                      : chunks <= 128 * 8 ? launch_rmsnorm<128, 8>
+                                          : launch_rmsnorm<256, 8>;
+  const cudaError_t e = launch(x, residual, weight, eps, M, d, residual_out, hidden_q,
+                               hidden_scale, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SIDBEAM_OK : cuda_error(e, "residual_rmsnorm_fp8: launch");
 }
 

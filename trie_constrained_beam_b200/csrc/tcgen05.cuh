@@ -149,7 +149,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
   tmem_wait_ld16(v);
 }
 
-// The same without the wait: several loads in flight, then one tmem_wait_ld.
+// 32 columns without the wait: several loads in flight, then a wait for each.
 __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t* v) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -162,9 +162,6 @@ __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t* v) {
         "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]),
         "=r"(v[31])
       : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_wait_ld() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 // The wait, tied to the registers that the loads filled: no use of them can move
 // before it.
