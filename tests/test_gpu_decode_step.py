@@ -155,3 +155,74 @@ def test_step_hidden_status_reaches_the_search(tcb, monkeypatch):
     search.step_hidden(0, head, x)
     assert tcb.sidbeam_get_device_status(search.workspace) == tcb.native.SIDBEAM_ERR_TIMEOUT
     assert tcb.sidbeam_get_device_status(search.workspace) == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_captured_decode_on_other_inputs(tcb, dtype):
+    """A captured decode replayed on inputs that it was not captured on, over buffers
+    filled with other values, gives every stage's bits of an eager decode on them."""
+    import torch
+    t16 = torch.bfloat16 if dtype == "bf16" else torch.float32
+    R, n, depth, V, H, Hkv, D, page = 3, 24, 3, 200, 4, 2, 64, 16
+    d = H * D
+    trie = tcb.sid_trie_build(host.draw_catalog(78, 4000, [V] * depth), [V] * depth)
+    g = torch.Generator(device="cuda").manual_seed(6)
+
+    def normal(*shape, s=1.0):
+        return (s * torch.randn(shape, device="cuda", generator=g)).to(torch.bfloat16)
+    search = tcb.BeamSearch(trie, R, n, V, depth=depth)
+    head = tcb.LmheadFp8(normal(V, d, s=0.2), 1 + normal(d, s=0.1), R * n, dtype=t16)
+    kc, vc = normal(R * 10, page, Hkv, D), normal(R * 10, page, Hkv, D)
+    table = torch.randperm(R * 10, device="cuda", generator=g).view(R, 10).to(torch.int32)
+    cache_len = torch.tensor([150, 33, 64], dtype=torch.int32, device="cuda")
+    embed, kv_embed = normal(V, H, D, s=1.5), normal(2, V, Hkv, D)
+    kb = torch.zeros((depth, R * n, Hkv, D), dtype=torch.bfloat16, device="cuda")
+    vb = torch.zeros_like(kb)
+    starts = [normal(R, H, D, s=1.5) for _ in range(2)]
+    start = starts[0].clone()
+    rows = [search.rows(t) for t in range(depth)]
+    q = [torch.empty((m, H, D), dtype=torch.bfloat16, device="cuda") for m in rows]
+    attn = [torch.empty_like(x) for x in q]
+    resid = [torch.empty((m, d), dtype=torch.bfloat16, device="cuda") for m in rows]
+    logits = [torch.empty((m, V), dtype=t16, device="cuda") for m in rows]
+
+    def decode():
+        q[0].copy_(start)
+        for t in range(depth):
+            if t:
+                code = search.bp_code[t - 1].reshape(-1).clamp_min(0).long()
+                q[t].copy_(embed[code])
+                kb[t - 1].copy_(kv_embed[0][code])
+                vb[t - 1].copy_(kv_embed[1][code])
+            search.attention(t, q[t], kc, vc, cache_len, attn[t], k_beam=kb, v_beam=vb,
+                             page_table=table)
+            search.step_hidden(t, head, attn[t].view(rows[t], d), residual=q[t].view(rows[t], d),
+                               residual_out=resid[t])
+            logits[t].copy_(head._logits[:rows[t], :V])
+        search.finalize()
+
+    outputs = (q + attn + resid + logits + [search.scores, search.bp_parent, search.bp_code,
+                                            search.nodes, search.sids, search.leaf])
+    eager = []
+    for s in starts:
+        start.copy_(s)
+        decode()
+        eager.append([x.clone() for x in outputs])
+    differ = [not torch.equal(a, b) for a, b in zip(*eager)]
+    assert all(differ[:-6]) and any(differ[-6:])
+    start.copy_(starts[0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        decode()
+    for which in (1, 0, 1):
+        for x in outputs + [kb, vb, head._logits]:
+            x.fill_(3)
+        head.hidden_q.view(torch.uint8).fill_(0x38)
+        head.hidden_scale.fill_(3)
+        start.copy_(starts[which])
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(eager[which], outputs)):
+            assert torch.equal(a, b), i
+    assert tcb.sidbeam_get_device_status(search.workspace) == 0

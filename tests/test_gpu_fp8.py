@@ -300,3 +300,49 @@ def test_head_made_on_a_side_stream(tcb):
     assert tcb.sidbeam_get_device_status(head.workspace, stream=side) == 0
     assert np.array_equal(_codes(head.w_q), _codes(want.w_q))
     assert torch.equal(head.w_scale, want.w_scale) and torch.equal(out, ref)
+
+
+@pytest.mark.parametrize("d", [272, 512, 528, 1024, 4112, 8192, 8208, 16368])
+def test_residual_rmsnorm_row_shapes(tcb, d):
+    """Hidden sizes at both ends of every count of threads and chunks a row."""
+    rng = np.random.default_rng(d)
+    M = 9
+    x, r = _bf16(rng.standard_normal((M, d))).cuda(), _bf16(2 * rng.standard_normal((M, d))).cuda()
+    w = _bf16(1 + 0.3 * rng.standard_normal(d)).cuda()
+    h64, y64 = ofp8.residual_rmsnorm(_f64(x), _f64(r), _f64(w), 1e-6)
+    ro, q, s = _norm_out(M, d)
+    tcb.residual_rmsnorm_fp8(x, r, w, 1e-6, ro, q, s)
+    assert np.all(np.abs(_f64(ro) - h64) <= (2.0 ** -8 + 2.0 ** -22) * np.abs(h64))
+    _check_quantised(y64, _codes(q), _f64(s), 1, (d + 16) * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("M,V,d", [(1300, 2050, 1040), (1300, 2177, 1040), (1281, 2303, 144),
+                                   (9473, 255, 64), (1152, 2304, 16)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_logits_wide_tiles_with_ragged_sides(tcb, M, V, d, dtype):
+    """Tiles of 256 codes, both output types: a codebook that ends in a tile's first or
+    second half (the other half has no column), rows and d that end inside a tile."""
+    import torch
+    t = torch.float32 if dtype == "f32" else torch.bfloat16
+    ops = _operands(M, V, d, M + V)
+    got = _logits(tcb, ops, V, t, pad=8)
+    _check_logits(got, ops, d, t)
+    assert torch.equal(got, _logits(tcb, ops, V, t, pad=8))
+
+
+@pytest.mark.parametrize("M,V,d", [(5, 256, 256), (20, 700, 2048), (16, 4096, 8192), (1300, 2050, 272)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_logits_rows_are_isolated_in_every_kernel(tcb, M, V, d, dtype):
+    """Infinite or NaN scales of a row stay in that row: few rows (their factors share a
+    table, their parts meet across a cluster) and wide tiles."""
+    import torch
+    t = torch.float32 if dtype == "f32" else torch.bfloat16
+    ops = list(_operands(M, V, d, 9 + M))
+    ref = _logits(tcb, ops, V, t).clone()
+    assert bool(torch.isfinite(ref).all())
+    ops[1] = ops[1].clone()
+    ops[1][2, 0], ops[1][M - 1, 1] = float("nan"), float("inf")
+    got = _logits(tcb, ops, V, t)
+    keep = [i for i in range(M) if i not in (2, M - 1)]
+    assert torch.equal(got[keep], ref[keep])
+    assert bool(torch.isnan(got[2]).all()) and not bool(torch.isfinite(got[M - 1]).any())

@@ -221,3 +221,27 @@ print("imported")
 """
     done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
     assert done.returncode == 0 and "imported" in done.stdout, done.stderr
+
+
+def test_oracle_norm_and_blocks_are_torchs():
+    """The norm against torch's own (float64), the block scales against the definition,
+    element by element."""
+    import torch
+    rng = np.random.default_rng(2)
+    x, res = rng.standard_normal((2, 5, 144)) * 3
+    w = rng.standard_normal(144)
+    for r in (None, res):
+        h, y = ofp8.residual_rmsnorm(x, r, w, 1e-3)
+        assert np.array_equal(h, x if r is None else x + r)
+        ref = torch.nn.functional.rms_norm(torch.from_numpy(h), (144,), torch.from_numpy(w), 1e-3)
+        assert np.allclose(y, ref.numpy(), rtol=1e-13, atol=0)
+    m = rng.standard_normal((130, 144))
+    m[128:] = 0
+    for rows in (1, 128):
+        s = ofp8.blocks(m, rows)
+        assert s.shape == (-(-130 // rows), 2)
+        full = ofp8.expand(s, rows, m.shape)
+        for i, j in ((0, 0), (5, 127), (127, 128), (128, 3), (129, 143)):
+            part = [abs(m[a, b]) for a in range(130) for b in range(144)
+                    if a // rows == i // rows and b // 128 == j // 128]
+            assert full[i, j] == max(max(part), 448 * 2.0 ** -100) / 448
