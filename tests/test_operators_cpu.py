@@ -245,3 +245,12 @@ def test_oracle_norm_and_blocks_are_torchs():
             part = [abs(m[a, b]) for a in range(130) for b in range(144)
                     if a // rows == i // rows and b // 128 == j // 128]
             assert full[i, j] == max(max(part), 448 * 2.0 ** -100) / 448
+
+
+def test_logits_refuse_rows_that_do_not_round_up(lib):
+    """The last 127 row counts of an int do not round up to whole tiles."""
+    def logits(M):
+        return lib.lmhead_logits_fp8(P(0x1000), P(0x2000), P(0x3000), P(0x4000), M, 8, 16,
+                                     P(0x5000), 0, 8, P(0x8000), 256, None)
+    for M in ((1 << 31) - 1, (1 << 31) - 127):
+        assert logits(M) == -1, M

@@ -587,7 +587,8 @@ extern "C" int lmhead_logits_fp8(const void* hidden_q, const float* hidden_scale
   if (M == 0) return SIDBEAM_OK;
   if (!hidden_q || !hidden_scale || !w_q || !w_scale || !logits)
     return set_error(SIDBEAM_ERR_INVALID_ARG, "lmhead_logits_fp8: NULL pointer argument");
-  if ((static_cast<int64_t>(M) + 127) / 128 * ((V + 127) / 128) > 0x3FFFFFFF)
+  if (M > 0x7FFFFFFF - kTileM ||
+      (static_cast<int64_t>(M) + 127) / 128 * ((V + 127) / 128) > 0x3FFFFFFF)
     return set_error(SIDBEAM_ERR_INVALID_ARG, "lmhead_logits_fp8: M=%d x V=%d too large", M, V);
   const int esize = dtype == SIDBEAM_BF16 ? 2 : 4;
   if (ld < V)
