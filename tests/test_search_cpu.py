@@ -105,3 +105,40 @@ def test_head_allocates_on_the_stream_it_quantises_on(calls, monkeypatch):
     made.clear()
     tcb.LmheadFp8(w, norm, 8)
     assert set(made) == {None}
+
+
+def test_search_steps_on_its_own_device(calls, monkeypatch):
+    """With another device current, attention and the 8-bit product run on the device of
+    their tensors; the constrained step and the end must follow them there (on the
+    current device they would read another device's memory, in no order)."""
+    entered, seen = [0], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            entered.append(self.index)
+
+        def __exit__(self, *exc):
+            entered.pop()
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: entered[-1])
+    for name in ("beam_step", "beam_step_gumbel", "beam_finalize"):
+        monkeypatch.setattr(native, name, lambda *a, _name=name, **kw: seen.append((_name, entered[-1])))
+    for temperature, step in ((0.0, "beam_step"), (0.5, "beam_step_gumbel")):
+        search, head = _search(temperature=temperature), _head()
+        search.device_index = 1
+        for t in range(2):
+            search.step_hidden(t, head, _rows(search.rows(t)))
+        search.step(1, head._logits)
+        search.finalize()
+        assert entered == [0]
+        assert seen == [(step, 1)] * 3 + [("beam_finalize", 1)]
+        seen.clear()
+    seen.clear()
+    search.device_index = 0     # already current: nothing is switched
+    monkeypatch.setattr(Device, "__enter__", None)
+    search.step(1, head._logits)
+    search.finalize()
+    assert [x[1] for x in seen] == [0, 0]

@@ -7,6 +7,8 @@ back-pointers straight into slice t of the [depth][R][n] history.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import native
@@ -96,6 +98,7 @@ class BeamSearch:
             if self.temperature > 0:
                 raise ValueError("widths with temperature > 0 is not supported")
             self.widths = torch.tensor(w, dtype=torch.int32, device=dev)
+        self.device_index = self.scores.get_device()
         self.sids = torch.empty((R, n, self.depth), dtype=torch.int32, device=dev)
         self.leaf = torch.empty((R, n), dtype=torch.int32, device=dev)
 
@@ -108,7 +111,18 @@ class BeamSearch:
             return self.root_scores, self.root_nodes, 1
         return self.scores[t - 1], self.nodes[t - 1], self.n
 
+    def _on_device(self):
+        """This search's device made current (the library launches there), as the calls
+        that take their device from their tensors do by themselves."""
+        if self.device_index < 0 or self.device_index == torch.cuda.current_device():
+            return contextlib.nullcontext()
+        return torch.cuda.device(self.device_index)
+
     def step(self, t: int, logits, stream=None):
+        with self._on_device():
+            self._step(t, logits, stream)
+
+    def _step(self, t: int, logits, stream):
         ps, pn, B_in = self.parents(t)
         if self.temperature > 0:
             native.beam_step_gumbel(self.trie, t, logits, ps, pn, self.R, B_in, self.n,
@@ -148,8 +162,9 @@ class BeamSearch:
         return native.beam_step_skipped_rows(self.workspace, stream=stream)
 
     def finalize(self, stream=None):
-        native.beam_finalize(self.depth, self.R, self.n, self.bp_parent, self.bp_code,
-                             self.nodes[self.depth - 1], self.sids, self.leaf, stream=stream)
+        with self._on_device():
+            native.beam_finalize(self.depth, self.R, self.n, self.bp_parent, self.bp_code,
+                                 self.nodes[self.depth - 1], self.sids, self.leaf, stream=stream)
         return self.sids, self.leaf, self.scores[self.depth - 1].view(self.R, self.n)
 
     def capture(self, logits_per_step, events=None):
