@@ -189,3 +189,30 @@ def test_two_graphs_share_a_workspace(tcb):
         torch.cuda.synchronize()
         assert torch.equal(a.out, ra) and torch.equal(b.out, rb)
     assert tcb.sidbeam_get_device_status(a.ws) == 0
+
+
+@pytest.mark.parametrize("H,Hkv,D", [(1, 1, 64), (16, 8, 128), (128, 1, 64)])
+@pytest.mark.parametrize("level", [1, 5, 16])
+def test_greedy_paths(tcb, H, Hkv, D, level):
+    """One beam a request: every level has one slot; a dead request among them."""
+    c = Case(6, 1, H, Hkv, D, [130, 0, 1, 300, 64, 17], level=level, seed=level + H)
+    c.bp[level - 1, 4, 0] = -1
+    _twice(tcb, c)
+    assert not c.out[4].any()
+
+
+@pytest.mark.parametrize("page", [0, 16])
+@pytest.mark.parametrize("B", [1, 140])
+def test_lengths_past_the_capacity_are_clamped(tcb, page, B):
+    import torch
+    c = Case(2, B, 2, 1, 64, [80, 64], page=page, seed=7, junk=False)
+    if page:
+        c.table = c.table[:, :5].contiguous()          # 80 tokens
+    else:
+        c.k, c.v = c.k[:, :80].contiguous(), c.v[:, :80].contiguous()
+    good = c.run(tcb).clone()
+    for n in (81, 1 << 30, 2 ** 31 - 1):
+        lens = torch.tensor([n, 64], dtype=torch.int32, device="cuda")
+        tcb.beam_attention(c.q, c.k, c.v, lens, c.out, c.ws, **c.kwargs())
+        assert tcb.sidbeam_get_device_status(c.ws) == tcb.native.SIDBEAM_ERR_DEVICE_CHECK
+        assert torch.equal(c.out, good)

@@ -346,3 +346,16 @@ def test_logits_rows_are_isolated_in_every_kernel(tcb, M, V, d, dtype):
     keep = [i for i in range(M) if i not in (2, M - 1)]
     assert torch.equal(got[keep], ref[keep])
     assert bool(torch.isnan(got[2]).all()) and not bool(torch.isfinite(got[M - 1]).any())
+
+
+def test_rmsnorm_in_place_of_x(tcb):
+    """residual_out in x's place, and x as its own residual."""
+    import torch
+    rng = np.random.default_rng(8)
+    x = _bf16(rng.standard_normal((6, 1040))).cuda()
+    w = _bf16(1 + 0.3 * rng.standard_normal(1040)).cuda()
+    h64, y64 = ofp8.residual_rmsnorm(_f64(x), _f64(x), _f64(w), 1e-6)
+    _, q, s = _norm_out(6, 1040)
+    tcb.residual_rmsnorm_fp8(x, x, w, 1e-6, x, q, s)
+    assert np.array_equal(_f64(x), h64)                # twice a bf16 value: exact
+    _check_quantised(y64, _codes(q), _f64(s), 1, (1040 + 16) * 2.0 ** -24)
