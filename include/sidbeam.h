@@ -345,7 +345,8 @@ int sidbeam_fused_lmhead_step(const sidbeam_trie* trie, int step, const void* hi
 
 /* residual_rmsnorm_fp8 -- the final norm of M rows, leaving them quantised:
  *   h = x + residual,  y = h / sqrt(mean_k h_k^2 + eps) * weight
- * in fp32 (y comes from the unrounded h).
+ * in fp32 (y comes from the unrounded h; the sum of h_k^2 within fp32's range, so
+ * |h_k| below 2^56, and above 2^-56 where eps is 0).
  *  x             device bf16 [M][d], row-major, 16-byte aligned.
  *  residual      device bf16 [M][d], or NULL (h = x).
  *  weight        device bf16 [d], 16-byte aligned.
@@ -367,8 +368,9 @@ int lmhead_quantize_fp8(const void* w_sid, int V, int d, void* w_q, float* w_sca
 /* lmhead_logits_fp8 -- lmhead_logits on quantised operands:
  *   logits[row][c] = sum_b hidden_scale[row][b] * w_scale[c / 128][b]
  *                          * sum_{k in block b} hidden_q[row][k] * w_q[c][k]
- * (tcgen05, exact products; each block's sum and the sum over blocks in fp32,
- * order not specified but the same for every call of the same shape).
+ * (tcgen05, exact products; each block's sum, the product of its two scales and the
+ * sum over blocks in fp32, and within its range; order not specified but the same
+ * for every call of the same shape).
  *  hidden_q     device e4m3 [M][d], hidden_scale device f32 [M][nb].
  *  w_q          device e4m3 [V][d], w_scale device f32 [ceil(V/128)][nb].
  *  logits       device [M][ld] of `dtype` (bf16: one rounding of the fp32 sum),
@@ -394,7 +396,9 @@ int lmhead_logits_fp8(const void* hidden_q, const float* hidden_scale, const voi
  * with the keys and values of head h / (H / Hkv). Products bf16 on the tensor
  * cores, scores, maxima, sums and the output's accumulation in fp32; the weights
  * of cached tokens are rounded to bf16 before they meet the values, the ancestors'
- * share of a row once to bf16 on its way to the output.
+ * share of a row once to bf16 on its way to the output. A row's sums are kept against
+ * a reference that its maximum may pass by up to 2^60 before they are scaled: finite
+ * values of 2^60 and more may overflow on the way.
  *  q            device bf16 [R*B][H][D]; a row starts q_row_stride elements after
  *               the one before (>= H*D, % 8 == 0, < 2^24; a slice of a wider
  *               projection is fine). Rows are request-major, row = r * B + b.

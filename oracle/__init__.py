@@ -32,7 +32,8 @@ candidates are padded with (-inf, -1, -1, -1).
 
 Parity status: every function here is pinned by ``tests/test_oracle_pins.py``
 (brute-force enumeration, library special cases, invariants, published
-generator vectors); none is "parity unpinned".
+generator vectors) or, for ``fp8`` and ``attention``, by
+``tests/test_operators_cpu.py``; none is "parity unpinned".
 """
 from .trie import OracleTrie  # noqa: F401
 from .beam import (  # noqa: F401

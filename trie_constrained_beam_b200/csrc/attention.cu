@@ -70,16 +70,19 @@ constexpr float kNegInf = -INFINITY;
 // units are split over the keys among the CTAs of a cluster instead, and joined
 // through distributed shared memory in rank order.
 //
-// What bounds it, measured with 16 query and 8 key heads of 128:
+// What bounds it, measured with 16 query and 8 key heads of 128. Two figures: at the
+// full clock of 1,965 MHz (some ms of calls after a pause), and in seconds of calls, where
+// the 1,000 W power cap lowers the clock (MHz in brackets):
 //  - Many rows, long prompts: the softmax, whose exponentials and conversions share
-//    their issue slots with the TMEM reads. 16 requests x 512 beams: 543 us over 8192
-//    tokens (1,013 TFLOP/s), 147 us over 2048, 82 us over 1024 (841), 26 us over 128.
-//  - Ancestors: 1024 tokens and 1, 2 or 4 levels take 100, 105 or 137 us against 82:
-//    each row gathers its own levels' keys and values, and the rows' warp groups
-//    take longer over them than the streams over the prompt.
-//  - One row a head (32 requests x 5000 tokens): the cache's bytes, 6.0 TB/s from
-//    pages of 64 (92% of the copy bandwidth).
-//  - One request, one row: latency. 128 tokens take 6.5 us, 1000 tokens 9.1.
+//    their issue slots with the TMEM reads. 16 requests x 512 beams: 540 us and 615 (1,732)
+//    over 8192 tokens (1,018 and 894 TFLOP/s), 148 and 166 (1,750) over 2048, 83 and 91
+//    (1,762) over 1024, 26 and 26 over 128.
+//  - Ancestors: 1024 tokens and 1, 2 or 4 levels take 101 and 111, 107 and 117, 137 and 142
+//    against 83 and 91: each row gathers its own levels' keys and values, and the rows'
+//    warp groups take longer over them than the streams over the prompt.
+//  - One row a head (32 requests x 5000 tokens): the cache's bytes, 6.1 TB/s and 5.4
+//    (1,600) from pages of 64 (94% and 83% of the copy bandwidth).
+//  - One request, one row: latency. 128 tokens take 6.0 us, 1000 tokens 8.9 (full clock).
 constexpr int kRows = 128;
 constexpr int kKeys = 128;
 constexpr int kMaxSplitLog2 = 3;
@@ -1184,9 +1187,11 @@ int launch_kernel(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& m
     }
   }
   // As few CTAs as end in the same number of rounds: the SMs left over would only
-  // compete for the cache's bytes early on. (32 rows of 2500-5000 tokens, 256 units:
-  // 88 us on 128 CTAs, 97 on 148, 95 with a CTA per unit; 64 x 128 beams, 512 units:
-  // 152, 160, 157.)
+  // compete for the cache's bytes early on. Against a CTA per SM, at full clock and in
+  // seconds of calls under the power cap: 32 rows of 2500-5000 tokens (256 units, 128 CTAs)
+  // 87 us and 94, against 98 and 102; all of 5000 107 and 121, against 109 and 122; 64 x 128
+  // beams over 1000-2000 tokens (512 units) 153 and 179, against 161 and 183; all of 2000
+  // 179 and 215 both ways.
   const int rounds = (a.units + sms - 1) / sms;
   const unsigned grid =
       static_cast<unsigned>(kSplit ? a.units * a.split : (a.units + rounds - 1) / rounds);
@@ -1211,8 +1216,10 @@ int launch_attention(AttnArgs& a, cudaStream_t stream) {
   a.units = static_cast<int>(units);
   const int64_t cap = a.table ? static_cast<int64_t>(a.table_stride) * a.page_size : a.page_size;
   const int64_t max_tiles = (cap + kKeys - 1) / kKeys;
-  // CTAs per unit: doubled while all clusters run at once and each CTA has a key tile.
-  // One row, 16 / 8 heads of 128, us on 1, 2, 4, 8 CTAs a unit:
+  // CTAs per unit: doubled while all clusters run at once and at most one CTA of a unit
+  // has no key tile (3 tiles on 4 CTAs, 7 on 8), by the capacity: the lengths are not
+  // known here. One row, 16 / 8 heads of 128, us at full clock on 1, 2, 4, 8 CTAs a unit
+  // (measured together; those chosen take 0.2 us less by now):
   //   384 tokens    9.4   9.5   8.5   8.9        1024   15.2  12.9   9.7   9.1
   //   512          10.2   9.6   8.6   9.1        2048   25.4  18.3  13.1  10.3
   // (256 tokens: 7.3, split 8.4.) Two rows of 2048: 25.4, 18.3, 13.4, and 19.8 on 8,
@@ -1339,8 +1346,9 @@ extern "C" int beam_attention(const sidbeam_attention* args, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // Two row tiles a unit where there are two: each key tile is read, and each page
   // of it asked for, once for 256 rows, and two warp groups see to the ancestors. For
-  // 16 x 512 beams, 1024 tokens (one tile a unit in brackets): 82 us (81), at 4 levels
-  // 137 (206), from pages of 16 88 (135); over 128 tokens 26 (31), over 8192 543 (519).
+  // 16 x 512 beams at full clock, 1024 tokens (one tile a unit in brackets): 82 us (81),
+  // at 4 levels 137 (206), from pages of 16 88 (135); over 128 tokens 26 (31), over 8192
+  // 543 (519).
   // More than 8 levels need the table space that one tile leaves.
   const bool dual = static_cast<int64_t>(B) * a.G > kRows && level <= 8;
   if (D == 64)

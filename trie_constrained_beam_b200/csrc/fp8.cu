@@ -59,15 +59,18 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
 // (16-byte loads; 16 neighbouring threads hold one scale block). The row stays
 // in registers between its sum of squares and its quantisation, so it is read
 // once: 7 bytes per element in all, the bound of this kernel (8192 rows of 2048:
-// 20.4 us, 89% of the copy bandwidth). T threads a row by its size (us per call at
-// 8192 or 16384 rows, T = 32 four rows to a CTA):
-//   d      256    512    1024   2048
-//   32     8.3   14.3    23.8   27.2
-//   128   17.0   20.5    24.6   22.6   (256 threads at 2048: 24.7)
+// 20.4 us at full clock, 89% of the copy bandwidth; 21.3 in seconds of calls, where the
+// power cap holds the clock at 1,777 MHz). T threads a row by its size (us per call at
+// full clock; up to d = 512 part of the inputs stays in L2, 16384 rows up to 1024, 8192
+// of 2048, 4096 above; T = 32: four rows to a CTA):
+//   d      256    512    1024   2048   4096   8192
+//   32     6.0   11.3    20.9   23.6
+//   128   17.2   18.1    20.5   20.2   21.3   41.4
+//   256                         21.4   20.9   40.4
 // up to 512 a warp wins, its shuffles being the whole sum; at 1024 the two are
-// level with many rows and 128 threads win with few (512 rows: 4.2 against 5.2);
-// above, a warp's registers hold too few rows in flight. 256 threads only where
-// 128 would need more than 8 chunks each.
+// level with many rows and 128 threads win with few (512 rows: 1.9 against 2.4);
+// above, a warp's registers hold too few rows in flight. 256 threads, level with 128 at
+// 4096 and 8192, only where 128 would need more than 8 chunks each.
 template <int T, int K>
 __global__ void __launch_bounds__(T == 32 ? 128 : T)
     rmsnorm_kernel(const uint4* x, const uint4* residual, const uint4* weight,
@@ -155,9 +158,10 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T)
 // ------------------------------------------------------------ weight quantisation
 // One CTA per block of 128 codes x 128 columns, kept in registers between its
 // maximum and its rounding: 16 threads per row, 16 rows per pass, 8 passes.
-// Bound by the 3 bytes per element it moves (8192 x 2048: 11.4 us, 68% of the copy
-// bandwidth: each CTA reads once and writes once, and 1024 of them are one wave
-// whose start and end count); a small weight (500 x 1040) by its 2 us of latency.
+// Bound by the 3 bytes per element it moves (8192 x 2048: 11.3 us, 68% of the copy
+// bandwidth, the same in seconds of calls: each CTA reads once and writes once, and 1024
+// of them are one wave whose start and end count); a small weight (500 x 1040) by its
+// 2 us of latency.
 constexpr int kQuantThreads = 256;
 
 __global__ void __launch_bounds__(kQuantThreads)

@@ -49,7 +49,9 @@ struct Fp8Args {
 // its way out: 128 KB of TMEM reads and 32K FMAs per SM; the epilogue keeps three
 // loads of 32 columns in turn, so that neither waits for the other.
 //
-// 4096 x 8192 x 2048 to fp32: 82-87 us, 1,600-1,680 TFLOP/s, half of the 8-bit rate.
+// 4096 x 8192 x 2048 to fp32: 84 us at the full clock of 1,965 MHz (1,630 TFLOP/s, half of
+// the 8-bit rate), 96.5 us in seconds of calls, where the 1,000 W power cap holds the
+// clock at 1,620 MHz (1,425 TFLOP/s); to bf16 74.5 and 85.5. The figures below are at full clock.
 // A block takes about 1,130 cycles, and a tile's store about 6,700 that overlap the
 // next tile's first blocks only. No unit is full: the tensor pipe 41%, issue slots
 // 48%, L2 26%, DRAM 18% of its rate; each SM takes in 48 KB a block, 43 bytes a
@@ -291,7 +293,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 //
 // Bound by the weight's bytes and the start and end of a call: 32 rows of
 // 8192 x 2048 take 7.5 us, a third of the copy bandwidth (2.7 us of bytes, about
-// 2 us for an empty kernel, then the first loads' and the cluster's latency).
+// 2 us for an empty kernel, then the first loads' and the cluster's latency). Few rows
+// do not reach the power cap: the figures here and at the rules on the host side hold
+// in seconds of calls too (but 15.7 us for the 15.1 of 512 rows).
 constexpr int kRowThreads = 192;  // TMA warp, MMA warp, 4 epilogue warps
 
 template <int NB>
