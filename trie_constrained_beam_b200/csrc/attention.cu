@@ -747,8 +747,10 @@ __global__ void __launch_bounds__(kDual ? 640 : 512, 1)
     // inside the products are free as long as both sides share them, so that each
     // lane reads whole 16-byte words. (One row per lane instead measured 4 times
     // the time: a lane's loads then touch 32 lines at once.) The weighted values,
-    // against the path's maximum, wait in the rows' places of the output (bf16);
-    // maximum and sum stay in the row's first two table entries.
+    // summed in fp32 against the path's maximum, wait in the rows' places of the output,
+    // rounded to bf16 once: two row tiles of D = 128 would take 128 KB in fp32, and 20 KB
+    // of shared memory are left. Maximum and sum stay, in fp32, in the row's first two
+    // table entries. (Error against 64 bits with 4 levels and with none: 0.0023.)
     auto attend_path = [&](const Unit& u, bool dead) {
       const int valid = rows_in(u);
       if (valid <= 0) return;
